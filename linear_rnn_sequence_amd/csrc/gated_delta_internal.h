@@ -1,0 +1,66 @@
+// Internal interface between the host entry points of the gated delta rule
+// (gated_delta_api.hip) and its kernel launchers.  Not installed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gated_delta.h"
+
+namespace gdr {
+
+// A checked problem: strides filled in, dense T, number of chunks.
+struct Problem {
+    const int *cu;  // nullptr: dense
+    int n_seq, T, total, slots;
+    int Hk, Hv, K, V;
+    long long q_stride, k_stride, v_stride;  // elements from token to token
+    const int *slots_in, *slots_out;
+    int pool;
+    float scale;
+    bool normalize, bf16;
+};
+
+struct ForwardArgs {
+    Problem p;
+    const void *q, *k, *v, *g, *beta;
+    const float *s0;
+    void *o;
+    float *s_out;
+    void *s_ckpt, *u;  // training: nullptr otherwise
+    char *records;     // workspace
+};
+
+struct BackwardArgs {
+    Problem p;
+    const void *q, *k, *v, *g, *beta, *d_o, *s_ckpt, *u;
+    const float *ds_T;
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float *ds0;
+    char *records;  // workspace: T^T, P^T and scalars of every chunk and value head
+    void *ds;       // workspace: [slots, Hv, V, K], cotangent of each chunk's exit state
+    void *dr;       // workspace: [total, Hv, V]
+};
+
+struct DecodeArgs {
+    Problem p;  // n_seq rows
+    const void *q, *k, *v, *g, *beta;
+    float *state;
+    void *o;
+};
+
+size_t forward_record_bytes(bool bf16);
+size_t backward_record_bytes(bool bf16);
+// values of one chain workgroup
+int chain_values(const Problem &p, bool backward);
+
+hipError_t launch_prep(const Problem &p, const void *q, const void *k, const void *g,
+                       const void *beta, char *records, bool backward, hipStream_t stream);
+hipError_t launch_forward(const ForwardArgs &a, hipStream_t stream);
+hipError_t launch_backward_chain(const BackwardArgs &a, hipStream_t stream);
+hipError_t launch_gradients(const BackwardArgs &a, hipStream_t stream);
+hipError_t launch_backward(const BackwardArgs &a, hipStream_t stream);
+hipError_t launch_decode(const DecodeArgs &a, hipStream_t stream);
+
+}  // namespace gdr
