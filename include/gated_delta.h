@@ -68,7 +68,7 @@ typedef struct {
     const int *cu_seqlens;  /* [n_seq + 1] on the device, or NULL: dense                 */
     int Hk, Hv, K, V;
     long long q_stride;     /* elements from one token's q to the next's; 0: Hk * K.     */
-    long long k_stride;     /*   A multiple of 16 bytes, at least Hk * K                 */
+    long long k_stride;     /*   A multiple of 16 bytes, at least Hk * K, at most 2^23   */
     long long v_stride;     /* likewise; 0: Hv * V                                       */
     const int *slots_in;    /* [n_seq] on the device, or NULL: state i                   */
     const int *slots_out;   /* likewise                                                  */

@@ -36,6 +36,7 @@ struct Sizes {
     size_t pool, states;     // float32 [pool, Hv, V, K], [n_seq, Hv, V, K]
     size_t ckpt;             // dt [slots, Hv, V, K]
     size_t fwd, bwd;         // workspaces
+    size_t fwd_seg;          // offset in the forward's
     size_t bwd_ds, bwd_dr;   // offsets in the backward's
 };
 
@@ -53,8 +54,6 @@ rwkv7_status check_problem(const gated_delta_problem *in, Problem &p, Sizes &z) 
         return RWKV7_ERR_SHAPE;
     if (!in->cu_seqlens && in->total % in->n_seq) return RWKV7_ERR_SHAPE;
     if ((!in->slots_in || !in->slots_out) && in->pool < in->n_seq) return RWKV7_ERR_SHAPE;
-    if ((long long)in->Hk * in->K > 0x7fffffffLL || (long long)in->Hv * in->V > 0x7fffffffLL)
-        return RWKV7_ERR_SHAPE;
     const int esz = in->dt == RWKV7_DT_BF16 ? 2 : 4;
     p = Problem{};
     p.cu = in->cu_seqlens;
@@ -67,15 +66,16 @@ rwkv7_status check_problem(const gated_delta_problem *in, Problem &p, Sizes &z) 
     if (slots > 0x7fffffffLL) return RWKV7_ERR_SHAPE;
     p.slots = (int)slots;
     const long long dense_k = (long long)p.Hk * p.K, dense_v = (long long)p.Hv * p.V;
-    p.q_stride = in->q_stride ? in->q_stride : dense_k;
-    p.k_stride = in->k_stride ? in->k_stride : dense_k;
-    p.v_stride = in->v_stride ? in->v_stride : dense_v;
-    const long long limit = (long long)1 << 40;  // elements from token to token
-    if (p.q_stride < dense_k || p.k_stride < dense_k || p.v_stride < dense_v ||
-        p.q_stride > limit || p.k_stride > limit || p.v_stride > limit)
+    const long long q_stride = in->q_stride ? in->q_stride : dense_k,
+                    k_stride = in->k_stride ? in->k_stride : dense_k,
+                    v_stride = in->v_stride ? in->v_stride : dense_v;
+    const long long limit = (long long)1 << 23;  // offsets inside a chunk fit 32 bits
+    if (q_stride < dense_k || k_stride < dense_k || v_stride < dense_v || q_stride > limit ||
+        k_stride > limit || v_stride > limit)
         return RWKV7_ERR_SHAPE;
-    if (p.q_stride * esz % 16 || p.k_stride * esz % 16 || p.v_stride * esz % 16)
+    if (q_stride * esz % 16 || k_stride * esz % 16 || v_stride * esz % 16)
         return RWKV7_ERR_ALIGN;
+    p.q_stride = (int)q_stride; p.k_stride = (int)k_stride; p.v_stride = (int)v_stride;
     p.slots_in = in->slots_in; p.slots_out = in->slots_out;
     p.pool = in->pool;
     p.scale = in->scale;
@@ -107,12 +107,15 @@ rwkv7_status check_problem(const gated_delta_problem *in, Problem &p, Sizes &z) 
     if (!mul_ok(z.fwd, (size_t)p.Hv) || !mul_ok(z.fwd, (size_t)p.slots) ||
         !mul_ok(rec, (size_t)p.Hv) || !mul_ok(rec, (size_t)p.slots))
         return RWKV7_ERR_SHAPE;
+    const Segments seg = plan_segments(p);
+    z.fwd_seg = up256(z.fwd);
+    if (seg.seg) z.fwd = z.fwd_seg + seg.state_bytes + seg.step_bytes;
     z.bwd_ds = up256(rec);
     z.bwd_dr = z.bwd_ds + up256(z.ckpt);
     z.bwd = z.bwd_dr + z.vd;
     // every grid's extent in threads fits 32 bits
     const size_t chains = (size_t)p.n_seq * p.Hv;
-    if (chains > 0xffffffffu / 256 / (p.V / 32) || (size_t)p.slots * p.Hk > 0xffffffffu / 256)
+    if (chains > 0xffffffffu / 512 / (p.V / 32) || (size_t)p.slots * p.Hk > 0xffffffffu / 1024)
         return RWKV7_ERR_SHAPE;
     return RWKV7_OK;
 }
@@ -182,6 +185,7 @@ rwkv7_status forward_impl(const gated_delta_problem *in, const void *q, const vo
     a.s_ckpt = train ? s_ckpt : nullptr;
     a.u = train ? u : nullptr;
     a.records = static_cast<char *>(workspace);
+    a.segments = a.records ? a.records + z.fwd_seg : nullptr;
     return launch_forward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? RWKV7_OK
                                                                              : RWKV7_ERR_HIP;
 }

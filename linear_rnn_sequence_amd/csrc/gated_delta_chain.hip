@@ -3,13 +3,13 @@
 //
 // Forward, per chunk with entry state S0 [V, K] and T, P of the preparation
 // kernel (c_t = exp(G_t)):
-//   R = diag(beta) (V - diag(c) K S0^T),  U = T R,
+//   R = V - diag(c) K S0^T,  U = T diag(beta) R,
 //   O = diag(scale c) Q S0^T + P U,       S_C = c_C S0 + U^T diag(c_C / c) K.
 // Backward, with D the cotangent of the chunk's exit state:
 //   dU = P^T dO + diag(c_C / c) K D^T,    dR = T^T dU,    dV = diag(beta) dR,
 //   dS0 = c_C D + scale dO^T diag(c) Q - dR^T diag(beta c) K.
 //
-// A wave owns 16 NT values (rows of the state) over all keys and needs nothing of
+// A wave owns 16 values (rows of the state) over all keys and needs nothing of
 // another wave: S^T lies in result tiles [keys, values], which are the right
 // operands of K S0^T and Q S0^T as they stand; R, U come out as [tokens,
 // values] tiles, the right operands of T R, P U and K^T U.  So a chunk is a
@@ -37,57 +37,55 @@ struct ChainArgs {
     void *out;     // o, or dv
     void *states;  // forward: s_ckpt or nullptr; backward: D of every chunk
     void *mid;     // forward: u or nullptr; backward: dR
-    long long q_stride, k_stride, v_stride;
+    int q_stride, k_stride, v_stride;
     int Hk, Hv, V, pool;
+    // segments: tokens of each (a multiple of 64), and per segment number and value
+    // head the state left by the segment, [V, K], and its transition, [parts, K, K]
+    int seg;
+    float *seg_state;
+    void *seg_step;
 };
-
-template <int K, int NT>
-struct State {
-    f32x4 t[K / 16][NT];
-};
-
-// state of (idx, hv): rows value0 + 16 n + lo, keys in tile_row order
-template <int K, int NT>
-__device__ __forceinline__ void load_state(State<K, NT> &s, const float *base, int g, int lo) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int ks = 0; ks < K / 32; ++ks)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s.t[2 * ks + h][n] = *reinterpret_cast<const f32x4 *>(
-                    base + (size_t)(16 * n + lo) * K + 32 * ks + 8 * g + 4 * h);
-}
-template <int K, int NT>
-__device__ __forceinline__ void store_state(const State<K, NT> &s, float *base, int g, int lo) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int ks = 0; ks < K / 32; ++ks)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<f32x4 *>(base + (size_t)(16 * n + lo) * K + 32 * ks + 8 * g +
-                                           4 * h) = s.t[2 * ks + h][n];
-}
-// the same rounded to E (the operand of the gradient kernel's products)
-template <class E, int K, int NT>
-__device__ __forceinline__ void store_rounded(const State<K, NT> &s, E *base, int g, int lo) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int ks = 0; ks < K / 32; ++ks) {
-            const Frag<E> f = to_frag<E>(s.t[2 * ks][n], s.t[2 * ks + 1][n]);
-            E *at = base + (size_t)(16 * n + lo) * K + 32 * ks + 8 * g;
-            if constexpr (sizeof(E) == 2) {
-                *reinterpret_cast<u32x4 *>(at) = f.v;
-            } else {
-                *reinterpret_cast<f32x4 *>(at) = f.v[0];
-                *reinterpret_cast<f32x4 *>(at + 4) = f.v[1];
-            }
-        }
-}
 
 __device__ __forceinline__ f32x4 zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+template <int K>
+struct State {
+    f32x4 t[K / 16];
+};
+
+template <int K>
+__device__ __forceinline__ void clear(State<K> &s) {
+#pragma unroll
+    for (int m = 0; m < K / 16; ++m) s.t[m] = zero();
+}
+// rows lo of the 16 at base, keys in tile_row order
+template <int K>
+__device__ __forceinline__ void load_state(State<K> &s, const float *base, int g, int lo) {
+#pragma unroll
+    for (int m = 0; m < K / 16; ++m)
+        s.t[m] = *reinterpret_cast<const f32x4 *>(base + lo * K + tile_row(m, 4 * g));
+}
+template <int K>
+__device__ __forceinline__ void store_state(const State<K> &s, float *base, int g, int lo) {
+#pragma unroll
+    for (int m = 0; m < K / 16; ++m)
+        *reinterpret_cast<f32x4 *>(base + lo * K + tile_row(m, 4 * g)) = s.t[m];
+}
+// the same rounded to E (the operand of the gradient kernel's products)
+template <class E, int K>
+__device__ __forceinline__ void store_rounded(const State<K> &s, E *base, int g, int lo) {
+#pragma unroll
+    for (int ks = 0; ks < K / 32; ++ks) {
+        const Frag<E> f = to_frag<E>(s.t[2 * ks], s.t[2 * ks + 1]);
+        E *at = base + lo * K + 32 * ks + 8 * g;
+        if constexpr (sizeof(E) == 2) {
+            *reinterpret_cast<u32x4 *>(at) = f.v;
+        } else {
+            *reinterpret_cast<f32x4 *>(at) = f.v[0];
+            *reinterpret_cast<f32x4 *>(at + 4) = f.v[1];
+        }
+    }
+}
 
 // index of a sequence's state in the pool, or -1
 __device__ __forceinline__ int slot_of(const int *slots, int i, int pool) {
@@ -95,392 +93,676 @@ __device__ __forceinline__ int slot_of(const int *slots, int i, int pool) {
     return s >= 0 && s < pool ? s : -1;
 }
 
-template <class E, int K, int NT, int W, bool TRAIN>
-__global__ __launch_bounds__(64 * W) void forward_chain_kernel(ChainArgs p) {
-    using Rec = FwdRecord<E>;
-    constexpr int kThreads = 64 * W, kValues = 16 * NT * W, KS = K / 32;
-    extern __shared__ __align__(16) char lds[];
-    Tile<E, K> tk{reinterpret_cast<E *>(lds)};
-    Tile<E, K> tq{reinterpret_cast<E *>(lds + tile_bytes<E, K>(kChunk))};
-    __shared__ Scalars sc;
-
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
-    const int parts = p.V / kValues;
-    const int part = (int)(blockIdx.x % parts);
-    const int hv = (int)(blockIdx.x / parts % p.Hv), seq = (int)(blockIdx.x / parts / p.Hv);
-    const int hk = hv / (p.Hv / p.Hk);
-    const int value0 = part * kValues + wave * 16 * NT;
-    const Seq sq = p.lay.seq(seq);
-    const size_t state_size = (size_t)p.V * K;
-
-    State<K, NT> S;
-    const int in = p.s_in ? slot_of(p.slots_in, seq, p.pool) : -1;
-    if (in >= 0) {
-        load_state(S, p.s_in + ((size_t)in * p.Hv + hv) * state_size + (size_t)value0 * K, g, lo);
+// Which (sequence or segment, value head, part of the values) a workgroup has.  Workgroups
+// go to the 8 XCDs (each with its own L2) in turn, so those that read the same
+// k and q rows, the parts of the value heads of one key head, are given numbers
+// that are equal modulo 8.
+struct Place {
+    int unit, hv, part;
+};
+__device__ __forceinline__ Place place_of(unsigned block, int Hk, int Hv, int parts) {
+    const unsigned members = (unsigned)(Hv / Hk * parts), groups = gridDim.x / members;
+    const unsigned whole = groups / 8 * 8 * members;
+    unsigned group, member;
+    if (block < whole) {
+        group = block / (8 * members) * 8 + block % 8;
+        member = block / 8 % members;
     } else {
-#pragma unroll
-        for (int m = 0; m < K / 16; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S.t[m][n] = zero();
+        group = groups / 8 * 8 + (block - whole) / members;
+        member = (block - whole) % members;
     }
-
-    const E *kp = static_cast<const E *>(p.k) + (long long)hk * K;
-    const E *qp = static_cast<const E *>(p.q) + (long long)hk * K;
-    const E *vp = static_cast<const E *>(p.v) + (long long)hv * p.V + value0 + lo;
-    const long long row = (long long)p.Hv * p.V;  // dense rows of o and u
-    E *op = static_cast<E *>(p.out) + (long long)hv * p.V + value0 + lo;
-    E *up = static_cast<E *>(p.mid) + (long long)hv * p.V + value0 + lo;
-
-    Stage<E, K, kChunk, kThreads> gk, gq;
-    const int len = sq.end - sq.begin;
-    if (len > 0) {
-        const int live = len < kChunk ? len : kChunk;
-        gk.load(kp + sq.begin * p.k_stride, p.k_stride, live, tid);
-        gq.load(qp + sq.begin * p.q_stride, p.q_stride, live, tid);
-    }
-    for (int c = 0; c * kChunk < len; ++c) {
-        const long long first = sq.begin + (long long)c * kChunk;
-        const int live = len - c * kChunk < kChunk ? len - c * kChunk : kChunk;
-        const size_t chunk_head = (size_t)(sq.slot0 + c) * p.Hv + hv;
-        const char *rec = p.records + chunk_head * Rec::kBytes;
-        if (c) __syncthreads();  // the last chunk's reads
-        gk.store(tk, tid);
-        gq.store(tq, tid);
-        for (int i = tid; i < (int)sizeof(Scalars) / 16; i += kThreads)
-            reinterpret_cast<u32x4 *>(&sc)[i] =
-                reinterpret_cast<const u32x4 *>(rec + Rec::kScalars)[i];
-        __syncthreads();
-        // this chunk's values and matrices, the next chunk's rows
-        f32x4 R[4][NT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = tile_row(i, 4 * g + e);
-                    R[i][n][e] = t < live ? to_float(vp[(first + t) * p.v_stride + 16 * n]) : 0.f;
-                }
-        Split<E> T[6];
-#pragma unroll
-        for (int f = 0; f < 6; ++f) T[f] = get_split<E>(rec + f * Rec::kSplitBytes, lane);
-        if ((c + 1) * kChunk < len) {
-            const int left = len - (c + 1) * kChunk, l2 = left < kChunk ? left : kChunk;
-            gk.load(kp + (first + kChunk) * p.k_stride, p.k_stride, l2, tid);
-            gq.load(qp + (first + kChunk) * p.q_stride, p.q_stride, l2, tid);
-        }
-        if (TRAIN)
-            store_rounded<E>(S, static_cast<E *>(p.states) + chunk_head * state_size +
-                                    (size_t)value0 * K, g, lo);
-
-        f32x4 O[4][NT];
-        {
-            f32x4 X[4][NT];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) X[i][n] = O[i][n] = zero();
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                Split<E> b[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    b[n] = to_split<E>(S.t[2 * ks][n], S.t[2 * ks + 1][n]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = tile_row(i, lo);
-                    const Frag<E> fk = tk.rows(r, 32 * ks, g), fq = tq.rows(r, 32 * ks, g);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        X[i][n] = mma(fk, b[n], X[i][n]);
-                        O[i][n] = mma(fq, b[n].hi, O[i][n]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = tile_row(i, 4 * g + e);
-                    const float be = sc.beta[t], ks = sc.kS[t], qs = sc.qS[t];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        R[i][n][e] = be * R[i][n][e] - ks * X[i][n][e];
-                        O[i][n][e] *= qs;
-                    }
-                }
-        }
-        f32x4 U[4][NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) U[i][n] = zero();
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const Split<E> b = to_split<E>(R[2 * st][n], R[2 * st + 1][n]);
-#pragma unroll
-                for (int f = 0; f < 6; ++f)
-                    if (kLowStep[f] == st) U[kLowTile[f]][n] = mma(T[f], b, U[kLowTile[f]][n]);
-            }
-        }
-        // the readout
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            Frag<E> b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = to_frag<E>(U[2 * st][n], U[2 * st + 1][n]);
-#pragma unroll
-            for (int f = 0; f < 6; ++f)
-                if (kLowStep[f] == st) {
-                    const Frag<E> a = get_frag<E>(rec + Rec::kP + f * Rec::kFragBytes, lane);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        O[kLowTile[f]][n] = mma(a, b[n], O[kLowTile[f]][n]);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = tile_row(i, 4 * g + e);
-                const float kd = sc.kD[t];
-                if (t < live)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        op[(first + t) * row + 16 * n] = from_float<E>(O[i][n][e]);
-                if (TRAIN && t < live)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        up[(first + t) * row + 16 * n] = from_float<E>(U[i][n][e]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) U[i][n][e] *= kd;
-            }
-        // the state
-        const float last = sc.last;
-#pragma unroll
-        for (int m = 0; m < K / 16; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S.t[m][n] *= last;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            Split<E> b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(U[2 * st][n], U[2 * st + 1][n]);
-#pragma unroll
-            for (int m = 0; m < K / 16; ++m) {
-                const Frag<E> a =
-                    tk.template cols<8>(32 * st, 32 * (m >> 1) + 4 * (m & 1), lane);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) S.t[m][n] = mma(a, b[n], S.t[m][n]);
-            }
-        }
-    }
-    if (p.s_out) {
-        const int out = slot_of(p.slots_out, seq, p.pool);
-        if (out >= 0)
-            store_state(S, p.s_out + ((size_t)out * p.Hv + hv) * state_size + (size_t)value0 * K,
-                        g, lo);
-    }
+    Place at;
+    at.unit = (int)(group / Hk);
+    at.hv = (int)(group % Hk) * (Hv / Hk) + (int)(member / parts);
+    at.part = (int)(member % parts);
+    return at;
 }
 
-template <class E, int K, int NT, int W>
-__global__ __launch_bounds__(64 * W) void backward_chain_kernel(ChainArgs p) {
-    using Rec = BwdRecord<E>;
-    constexpr int kThreads = 64 * W, kValues = 16 * NT * W, KS = K / 32;
-    extern __shared__ __align__(16) char lds[];
-    Tile<E, K> tk{reinterpret_cast<E *>(lds)};
-    Tile<E, K> tq{reinterpret_cast<E *>(lds + tile_bytes<E, K>(kChunk))};
-    Tile<E, kValues> to{reinterpret_cast<E *>(lds + 2 * tile_bytes<E, K>(kChunk))};
-    __shared__ Scalars sc;
+// Shared memory of a forward workgroup of W waves: two buffers with a chunk's k and q
+// rows and its record (bf16) or the record's scalars (float), and each wave's
+// values.
+template <class E, int K, int W>
+struct ForwardLds {
+    static constexpr int kThreads = 64 * W;
+    static constexpr int kTile = tile_bytes<E, K>(kChunk);
+    static constexpr bool kRecord = sizeof(E) == 2;
+    static constexpr int kRecPer = (FwdRecord<E>::kBytes + 16 * kThreads - 1) / (16 * kThreads);
+    static constexpr int kRest = kRecord ? kRecPer * 16 * kThreads : kScalarSpace;
+    static constexpr int kBuffer = 2 * kTile + kRest;
+    static constexpr int kValueTile = tile_bytes<E, 16>(kChunk);
+    static constexpr int kBytes = 2 * kBuffer + W * kValueTile;
+    static_assert(kBytes <= 160 * 1024, "fits a CU");
+    static_assert(kRecord || kThreads == 256, "a float of each thread");
+};
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
-    const int parts = p.V / kValues;
-    const int part = (int)(blockIdx.x % parts);
-    const int hv = (int)(blockIdx.x / parts % p.Hv), seq = (int)(blockIdx.x / parts / p.Hv);
-    const int hk = hv / (p.Hv / p.Hk);
-    const int value0 = part * kValues + wave * 16 * NT;
-    const Seq sq = p.lay.seq(seq);
+enum Mode { kInfer, kTrain, kSummary };
+
+// The chunks' shared rows are double-buffered in shared memory: while the waves work
+// on chunk c, the rows of c + 1 go from registers to the other buffer and those
+// of c + 2 are on their way to the registers.  In bf16 the chunk's record (T, P
+// and scalars) goes the same way; waves that each loaded T and P for themselves
+// kept the CU's vector cache busy longer than its matrix cores.  In float the
+// record does not fit, and the products take so long that the loads do not
+// matter.  So a load has about one chunk's time to arrive, and a chunk needs one
+// barrier.  Loads of chunks behind the last one are buffer accesses out of range.
+//
+// A workgroup takes a whole sequence, or one segment of it (p.seg): kSummary only
+// carries the state over a segment, from zeros (from the sequence's state for its
+// first one), for p.V / (16 W) parts; the parts behind those start from the
+// rows of the unit matrix and see no values, which gives the segment's
+// transition S0 -> S0 M.  combine_kernel turns these into the states at the
+// segments' starts, from which the segments are then done in parallel.
+template <class E, int K, int W, Mode MODE>
+__global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_kernel(
+    ChainArgs p) {
+    using Rec = FwdRecord<E>;
+    using L = ForwardLds<E, K, W>;
+    constexpr int KS = K / 32, kTile = L::kTile, kBuffer = L::kBuffer, kThreads = 64 * W;
+    constexpr int kValues = 16 * W, NT = 1;
+    extern __shared__ __align__(16) char lds[];
+
+    const int tid = threadIdx.x, lane = tid & 63,
+              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
+    const int v_parts = p.V / kValues;
+    const Place at = place_of(blockIdx.x, p.Hk, p.Hv,
+                              v_parts + (MODE == kSummary ? (K + kValues - 1) / kValues : 0));
+    const int hv = at.hv, hk = hv / (p.Hv / p.Hk);
+    const bool step = MODE == kSummary && at.part >= v_parts;  // a part of the transition
+    const int value0 = (step ? at.part - v_parts : at.part) * kValues + wave * 16 * NT;
     const size_t state_size = (size_t)p.V * K;
 
-    State<K, NT> D;
-    const size_t state_at = ((size_t)seq * p.Hv + hv) * state_size + (size_t)value0 * K;
-    if (p.s_in) {
-        load_state(D, p.s_in + state_at, g, lo);
-    } else {
+    // the sequence, and this workgroup's chunks c0 .. c0 + chunks - 1 of it
+    Seq sq;
+    int seq = at.unit, first = 0, seg_slot = 0, seg_last = 0;
+    bool last_part = true;
+    if (p.seg) {
+        seq = p.lay.find(at.unit, p.seg, sq);
+        seg_slot = at.unit;
+        const long long ahead = (long long)(at.unit - sq.slot0) * p.seg;
+        if (at.unit < sq.slot0 || (ahead >= sq.end - sq.begin && ahead > 0)) return;
+        first = (int)ahead;
+        seg_last = sq.slot0 + (sq.end - sq.begin - 1) / p.seg;
+        last_part = sq.end - sq.begin - first <= p.seg;
+        if (MODE == kSummary && (last_part || (step && first == 0))) return;
+    }
+    sq = p.lay.seq(seq, kChunk);
+    const int c0 = first / kChunk;
+    const int rest = sq.end - sq.begin - first, len = p.seg && rest > p.seg ? p.seg : rest;
+    const int chunks = (len + kChunk - 1) / kChunk;
+    const long long token = (long long)sq.begin + first;
+
+    // The start: of a sequence (kept in the place of its last segment's summary, which
+    // nothing needs, since s_out may be s_in: the last segment may be done before
+    // the first one starts), of a later segment, or zeros.
+    State<K> S[NT];
+    const float *from = nullptr;
+    if (MODE != kSummary && !last_part && !first)
+        from = p.seg_state + ((size_t)seg_last * p.Hv + hv) * state_size;
+    else if (MODE != kSummary && first)
+        from = p.seg_state + ((size_t)(seg_slot - 1) * p.Hv + hv) * state_size;
+    else if (p.s_in && !first && !step) {
+        const int in = slot_of(p.slots_in, seq, p.pool);
+        if (in >= 0) from = p.s_in + ((size_t)in * p.Hv + hv) * state_size;
+    }
 #pragma unroll
-        for (int m = 0; m < K / 16; ++m)
+    for (int n = 0; n < NT; ++n) {
+        if (from) {
+            load_state(S[n], from + (size_t)(value0 + 16 * n) * K, g, lo);
+        } else {
+            clear(S[n]);
+            if (step)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) D.t[m][n] = zero();
+                for (int m = 0; m < K / 16; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[n].t[m][e] = tile_row(m, 4 * g + e) == value0 + 16 * n + lo ? 1.f : 0.f;
+        }
     }
 
-    const long long row = (long long)p.Hv * p.V;
-    const E *kp = static_cast<const E *>(p.k) + (long long)hk * K;
-    const E *qp = static_cast<const E *>(p.q) + (long long)hk * K;
-    const E *dop = static_cast<const E *>(p.v) + (long long)hv * p.V + part * kValues;
-    E *dvp = static_cast<E *>(p.out) + (long long)hv * p.V + value0 + lo;
-    E *drp = static_cast<E *>(p.mid) + (long long)hv * p.V + value0 + lo;
+    if (MODE == kSummary && !first)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            store_state(S[n], p.seg_state + ((size_t)seg_last * p.Hv + hv) * state_size +
+                                  (size_t)(value0 + 16 * n) * K, g, lo);
 
-    const int len = sq.end - sq.begin;
-    const int chunks = (len + kChunk - 1) / kChunk;
-    Stage<E, K, kChunk, kThreads> gk, gq;
-    Stage<E, kValues, kChunk, kThreads> go;
-    auto fetch = [&](int c) {
-        const long long first = sq.begin + (long long)c * kChunk;
-        const int live = len - c * kChunk < kChunk ? len - c * kChunk : kChunk;
-        gk.load(kp + first * p.k_stride, p.k_stride, live, tid);
-        gq.load(qp + first * p.q_stride, p.q_stride, live, tid);
-        go.load(dop + first * row, row, live, tid);
+    const E *kp = static_cast<const E *>(p.k) + token * p.k_stride + hk * K;
+    const E *qp = static_cast<const E *>(p.q) + token * p.q_stride + hk * K;
+    const E *vp = static_cast<const E *>(p.v) + token * p.v_stride + hv * p.V + (step ? 0 : value0);
+    const int row = p.Hv * p.V;  // dense rows of o and u
+    E *op = static_cast<E *>(p.out) + token * row + hv * p.V + value0;
+    E *up = static_cast<E *>(p.mid) + token * row + hv * p.V + value0;
+    const size_t rec_step = (size_t)p.Hv * Rec::kBytes;
+    const char *rec = p.records + ((size_t)(sq.slot0 + c0) * p.Hv + hv) * Rec::kBytes;
+    E *states = static_cast<E *>(p.states) +
+                ((size_t)(sq.slot0 + c0) * p.Hv + hv) * state_size + (size_t)value0 * K;
+    const Tile<E, 16 * NT> tv{reinterpret_cast<E *>(lds + 2 * kBuffer + wave * L::kValueTile)};
+
+    auto live_of = [&](int c) {
+        const int left = len - c * kChunk;
+        return left < kChunk ? left : kChunk;  // none or fewer: nothing is in range
     };
-    if (chunks > 0) fetch(chunks - 1);
-    for (int c = chunks - 1; c >= 0; --c) {
-        const long long first = sq.begin + (long long)c * kChunk;
-        const int live = len - c * kChunk < kChunk ? len - c * kChunk : kChunk;
-        const size_t chunk_head = (size_t)(sq.slot0 + c) * p.Hv + hv;
-        const char *rec = p.records + chunk_head * Rec::kBytes;
-        if (c != chunks - 1) __syncthreads();
-        gk.store(tk, tid);
-        gq.store(tq, tid);
-        go.store(to, tid);
-        for (int i = tid; i < (int)sizeof(Scalars) / 16; i += kThreads)
-            reinterpret_cast<u32x4 *>(&sc)[i] =
-                reinterpret_cast<const u32x4 *>(rec + Rec::kScalars)[i];
-        __syncthreads();
-        if (c > 0) fetch(c - 1);
-        store_rounded<E>(D, static_cast<E *>(p.states) + chunk_head * state_size +
-                                (size_t)value0 * K, g, lo);
+    auto buffer = [&](int c) { return lds + (c & 1) * kBuffer; };
 
-        // dU = diag(c_C / c) K D^T + P^T dO
-        f32x4 X[4][NT];
+    Stage<E, K, kChunk, kThreads> gk, gq;
+    Stage<E, 16 * NT, kChunk, 64> gv;  // this wave's values
+    u32x4 gr[L::kRecPer];
+    float gs = 0.f, last_next = 0.f;
+    auto fetch_rows = [&](int c) {
+        const int live = live_of(c);
+        gk.load(kp + (long long)c * kChunk * p.k_stride, p.k_stride, live, tid);
+        if (MODE != kSummary)
+            gq.load(qp + (long long)c * kChunk * p.q_stride, p.q_stride, live, tid);
+        const char *r = rec + c * rec_step;
+        if constexpr (L::kRecord) {
+            const Buffer b(r, c < chunks ? Rec::kBytes : 0);
+#pragma unroll
+            for (int i = 0; i < L::kRecPer; ++i) gr[i] = b.load16((tid + i * kThreads) * 16);
+        } else {
+            gs = Buffer(r + Rec::kScalars, c < chunks ? kScalarSpace : 0).load_float(tid * 4);
+        }
+    };
+    auto put_rows = [&](int c) {
+        char *b = buffer(c);
+        gk.store(Tile<E, K>{reinterpret_cast<E *>(b)}, tid);
+        if (MODE != kSummary) gq.store(Tile<E, K>{reinterpret_cast<E *>(b + kTile)}, tid);
+        if constexpr (L::kRecord) {
+#pragma unroll
+            for (int i = 0; i < L::kRecPer; ++i)
+                *reinterpret_cast<u32x4 *>(b + 2 * kTile + (tid + i * kThreads) * 16) = gr[i];
+        } else {
+            reinterpret_cast<float *>(b + 2 * kTile)[tid] = gs;
+        }
+    };
+    auto fetch_values = [&](int c) {
+        gv.load(vp + (long long)c * kChunk * p.v_stride, p.v_stride, step ? 0 : live_of(c), lane);
+        if constexpr (!L::kRecord)
+            last_next = Buffer(rec + c * rec_step + Rec::kScalars + kScalarSpace, c < chunks ? 4 : 0)
+                            .load_float(0);
+    };
+    Split<E> T[6];
+    Frag<E> P[6];
+    auto fetch_T = [&](int c) {
+        const char *src = rec + c * rec_step;
+#pragma unroll
+        for (int f = 0; f < 6; ++f) T[f] = get_split<E>(src + f * Rec::kSplitBytes, lane);
+    };
+    auto fetch_P = [&](int c) {
+        const char *src = rec + c * rec_step + Rec::kP;
+#pragma unroll
+        for (int f = 0; f < 6; ++f) P[f] = get_frag<E>(src + f * Rec::kFragBytes, lane);
+    };
+    if (chunks > 0) {
+        fetch_rows(0);
+        put_rows(0);
+        // in the loop's order, and as many accesses behind the rows' loads, so that the
+        // loop waits for no more than it needs
+        fetch_rows(1);
+        fetch_values(0);
+        if (MODE != kSummary) {
+            const Buffer none(op, 0);
+#pragma unroll
+            for (int i = 0; i < 4 * NT; ++i) none.store4(0, zero(), E());
+        }
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int live = live_of(c);
+        __syncthreads();  // buffer c is whole, and the other one has been read
+        put_rows(c + 1);
+        if constexpr (!L::kRecord) fetch_T(c);
+        fetch_rows(c + 2);
+        const char *buf = buffer(c);
+        const Tile<E, K> tk{reinterpret_cast<E *>(const_cast<char *>(buf))},
+            tq{reinterpret_cast<E *>(const_cast<char *>(buf) + kTile)};
+        const char *rc = buf + 2 * kTile;
+        const Scalars &sc = *reinterpret_cast<const Scalars *>(L::kRecord ? rc + Rec::kScalars : rc);
+        gv.store(tv, lane);  // read by this wave alone
+        const float last = L::kRecord ? sc.last : last_next;
+        const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)];
+        fetch_values(c + 1);
+        if (MODE == kTrain)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                store_rounded<E>(S[n], states + (size_t)c * p.Hv * state_size + 16 * n * K, g, lo);
+
+        // X = K S0^T [tokens, values]; O^T = S0 Q^T [values, tokens], so that a lane
+        // ends up with four neighbouring values of a token
+        f32x4 X[4][NT], O[4][NT], R[4][NT];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) X[i][n] = zero();
+            for (int n = 0; n < NT; ++n) X[i][n] = O[i][n] = zero();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             Split<E> b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(D.t[2 * ks][n], D.t[2 * ks + 1][n]);
+            Frag<E> fk[4], fq[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const Frag<E> fk = tk.rows(tile_row(i, lo), 32 * ks, g);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) X[i][n] = mma(fk, b[n], X[i][n]);
+                fk[i] = tk.rows(tile_row(i, lo), 32 * ks, g);
+                if (MODE != kSummary) fq[i] = tq.rows(tile_row(i, lo), 32 * ks, g);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(S[n].t[2 * ks], S[n].t[2 * ks + 1]);
+#pragma unroll
+            for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        X[i][n] = mma_mixed(part, fk[i], b[n], X[i][n]);
+            if (MODE != kSummary)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) O[i][n] = mma(b[n].hi, fq[i], O[i][n]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float kd = sc.kD[tile_row(i, 4 * g + e)];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) X[i][n][e] *= kd;
-            }
-        Frag<E> fo[2][NT];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                fo[st][n] = to.template cols<4>(32 * st, wave * 16 * NT + 16 * n, lane);
-#pragma unroll
-        for (int f = 0; f < 6; ++f) {
-            const Split<E> a = get_split<E>(rec + Rec::kP + f * Rec::kSplitBytes, lane);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                X[kUpTile[f]][n] = mma(a, fo[kUpStep[f]][n], X[kUpTile[f]][n]);
-        }
-        // dR = T^T dU
-        f32x4 R[4][NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) R[i][n] = zero();
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const Split<E> b = to_split<E>(X[2 * st][n], X[2 * st + 1][n]);
-#pragma unroll
-                for (int f = 0; f < 6; ++f)
-                    if (kUpStep[f] == st)
-                        R[kUpTile[f]][n] =
-                            mma(get_split<E>(rec + f * Rec::kSplitBytes, lane), b, R[kUpTile[f]][n]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = tile_row(i, 4 * g + e);
-                const float be = sc.beta[t], ks = -sc.kS[t];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (t < live) {
-                        drp[(first + t) * row + 16 * n] = from_float<E>(R[i][n][e]);
-                        dvp[(first + t) * row + 16 * n] = from_float<E>(be * R[i][n][e]);
-                    }
-                    R[i][n][e] *= ks;
-                }
-            }
-        // dS0 = c_C D + dO^T diag(scale c / |q|) Q - dR^T diag(beta c / |k|) K
-        const float last = sc.last;
-#pragma unroll
-        for (int m = 0; m < K / 16; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) D.t[m][n] *= last;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            Split<E> b[NT], bo[NT];
+        for (int i = 0; i < 4; ++i) {
+            const float qs = sc.qS[tile_row(i, lo)];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                b[n] = to_split<E>(R[2 * st][n], R[2 * st + 1][n]);
-                f32x4 x0, x1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x0[e] = fo[st][n].at(e) * sc.qS[32 * st + 8 * g + e];
-                    x1[e] = fo[st][n].at(4 + e) * sc.qS[32 * st + 8 * g + 4 + e];
-                }
-                bo[n] = to_split<E>(x0, x1);
+                R[i][n] = tv.template column4<4>(tile_row(i, 4 * g), 16 * n, lane) +
+                          row_bcast4(kS, i) * X[i][n];
+                if (MODE != kSummary) O[i][n] *= qs;
             }
+        }
+        if constexpr (!L::kRecord && MODE != kSummary) fetch_P(c);
+        f32x4 U[4][NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) U[i][n] = zero();
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            Split<E> b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(R[2 * st][n], R[2 * st + 1][n]);
+            if constexpr (L::kRecord)
+#pragma unroll
+                for (int f = 0; f < 6; ++f)
+                    if (kLowStep[f] == st) T[f] = get_split<E>(rc + f * Rec::kSplitBytes, lane);
+#pragma unroll
+            for (int part = 0; part < kPartsSplit<E>; ++part)
+#pragma unroll
+                for (int f = 0; f < 6; ++f)
+                    if (kLowStep[f] == st)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            U[kLowTile[f]][n] = mma_split(part, T[f], b[n], U[kLowTile[f]][n]);
+        }
+        // the state
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < K / 16; ++m) S[n].t[m] *= last;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            Split<E> b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                b[n] = to_split<E>(row_bcast4(kD, 2 * st) * U[2 * st][n],
+                                   row_bcast4(kD, 2 * st + 1) * U[2 * st + 1][n]);
+#pragma unroll
+            for (int half = 0; half < K / 64; ++half) {  // four tiles of keys at a time
+                Frag<E> a[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    a[m] = tk.template cols<8>(32 * st, 64 * half + 32 * (m >> 1) + 4 * (m & 1), lane);
+#pragma unroll
+                for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            S[n].t[4 * half + m] = mma_mixed(part, a[m], b[n], S[n].t[4 * half + m]);
+            }
+        }
+        if (MODE != kSummary) {
+            // the readout: O^T += U^T P^T
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                Frag<E> b[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) b[n] = to_frag<E>(U[2 * st][n], U[2 * st + 1][n]);
+#pragma unroll
+                for (int f = 0; f < 6; ++f)
+                    if (kLowStep[f] == st) {
+                        if constexpr (L::kRecord)
+                            P[f] = get_frag<E>(rc + Rec::kP + f * Rec::kFragBytes, lane);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            O[kLowTile[f]][n] = mma(b[n], P[f], O[kLowTile[f]][n]);
+                    }
+            }
+            const Buffer bo(op + (long long)c * kChunk * row, row_bytes<E>(live, row));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    bo.store4((unsigned)(tile_row(i, lo) * row + 16 * n + 4 * g) *
+                                  (unsigned)sizeof(E), O[i][n], E());
+        }
+        if (MODE == kTrain) {
+            const Buffer bu(up + (long long)c * kChunk * row, row_bytes<E>(live, row));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bu.store1((unsigned)(tile_row(i, 4 * g + e) * row + 16 * n + lo) *
+                                      (unsigned)sizeof(E), U[i][n][e], E());
+        }
+    }
+    float *to = nullptr;
+    if (MODE == kSummary) {
+        if (step) {  // the transition's rows, as the operand planes of combine_kernel
+            constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
+            E *plane = static_cast<E *>(p.seg_step) +
+                       ((size_t)seg_slot * p.Hv + hv) * (kPlanes * K * K) + (size_t)value0 * K;
+            if (value0 < K)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    store_rounded<E>(S[n], plane + 16 * n * K, g, lo);
+                    if constexpr (kPlanes == 2) {
+                        State<K> low;
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            const Frag<E> hi = to_frag<E>(S[n].t[2 * ks], S[n].t[2 * ks + 1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                low.t[2 * ks][e] = S[n].t[2 * ks][e] - hi.at(e);
+                                low.t[2 * ks + 1][e] = S[n].t[2 * ks + 1][e] - hi.at(4 + e);
+                            }
+                        }
+                        store_rounded<E>(low, plane + K * K + 16 * n * K, g, lo);
+                    }
+                }
+            return;
+        }
+        to = p.seg_state + ((size_t)seg_slot * p.Hv + hv) * state_size;
+    } else if (p.s_out && last_part) {
+        const int out = slot_of(p.slots_out, seq, p.pool);
+        if (out >= 0) to = p.s_out + ((size_t)out * p.Hv + hv) * state_size;
+    }
+    if (to)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) store_state(S[n], to + (size_t)(value0 + 16 * n) * K, g, lo);
+}
+
+// From the segments' summaries to the states at their ends, in place: the state
+// left by segment j - 1 times the transition of segment j, plus what segment j
+// leaves from zeros.  One workgroup per sequence, value head and 64 values, a wave
+// per 16; the next transition is loaded while this one is multiplied.
+constexpr int kThreads = 256;  // of the kernels below: four waves
+
+template <class E, int K>
+__global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
+    constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63,
+              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
+    const Place at = place_of(blockIdx.x, p.Hk, p.Hv, p.V / 64);
+    const Seq sq = p.lay.seq(at.unit, p.seg);
+    const int segments = (sq.end - sq.begin + p.seg - 1) / p.seg;
+    if (segments < 3) return;  // the first segment's summary is the second's state already
+    const size_t state_size = (size_t)p.V * K;
+    float *state = p.seg_state + ((size_t)sq.slot0 * p.Hv + at.hv) * state_size +
+                   (size_t)(at.part * 64 + wave * 16) * K;
+    const E *step = static_cast<const E *>(p.seg_step) +
+                    ((size_t)sq.slot0 * p.Hv + at.hv) * (kPlanes * K * K);
+    const Tile<E, K> tm[2] = {Tile<E, K>{reinterpret_cast<E *>(lds)},
+                              Tile<E, K>{reinterpret_cast<E *>(lds + tile_bytes<E, K>(K))}};
+    Stage<E, K, K, kThreads> gm[kPlanes];
+    State<K> S, next;
+    load_state(S, state, g, lo);
+    auto fetch = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < kPlanes; ++x)
+            gm[x].load(step + (size_t)j * p.Hv * (kPlanes * K * K) + x * K * K, K,
+                       j < segments - 1 ? K : 0, tid);
+        if (j < segments - 1) load_state(next, state + (size_t)j * p.Hv * state_size, g, lo);
+    };
+    fetch(1);
+    for (int j = 1; j < segments - 1; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kPlanes; ++x) gm[x].store(tm[x], tid);
+        __syncthreads();
+        State<K> R = next;
+        fetch(j + 1);
+#pragma unroll
+        for (int ks = 0; ks < K / 32; ++ks) {
+            const Split<E> b = to_split<E>(S.t[2 * ks], S.t[2 * ks + 1]);
 #pragma unroll
             for (int m = 0; m < K / 16; ++m) {
                 const int col = 32 * (m >> 1) + 4 * (m & 1);
-                const Frag<E> ak = tk.template cols<8>(32 * st, col, lane);
-                const Frag<E> aq = tq.template cols<8>(32 * st, col, lane);
+                Split<E> a;
+                a.hi = tm[0].template cols<8>(32 * ks, col, lane);
+                if constexpr (kPlanes == 2) a.lo = tm[1].template cols<8>(32 * ks, col, lane);
+                R.t[m] = mma(a, b, R.t[m]);
+            }
+        }
+        S = R;
+        store_state(S, state + (size_t)j * p.Hv * state_size, g, lo);
+    }
+}
+
+constexpr int kValues = 64;  // values of a backward workgroup: 16 a wave
+
+// The same pipeline backwards: the rows of k, q and dO double-buffered, T^T and
+// P^T loaded again as soon as they have been used.
+template <class E, int K>
+__global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p) {
+    using Rec = BwdRecord<E>;
+    constexpr int KS = K / 32, kTile = tile_bytes<E, K>(kChunk);
+    constexpr int kBuffer = 2 * kTile + kScalarSpace;
+    extern __shared__ __align__(16) char lds[];
+
+    const int tid = threadIdx.x, lane = tid & 63,
+              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
+    const Place at = place_of(blockIdx.x, p.Hk, p.Hv, p.V / kValues);
+    const int hv = at.hv, hk = hv / (p.Hv / p.Hk);
+    const int value0 = at.part * kValues + wave * 16;
+    const Seq sq = p.lay.seq(at.unit, kChunk);
+    const int len = sq.end - sq.begin, chunks = (len + kChunk - 1) / kChunk;
+    const size_t state_size = (size_t)p.V * K;
+    const Tile<E, 16> to{reinterpret_cast<E *>(lds + 2 * kBuffer) + wave * kChunk * 16};
+
+    State<K> D;
+    const size_t state_at = ((size_t)at.unit * p.Hv + hv) * state_size + (size_t)value0 * K;
+    if (p.s_in)
+        load_state(D, p.s_in + state_at, g, lo);
+    else
+        clear(D);
+
+    const int row = p.Hv * p.V;
+    const E *kp = static_cast<const E *>(p.k) + (long long)sq.begin * p.k_stride + hk * K;
+    const E *qp = static_cast<const E *>(p.q) + (long long)sq.begin * p.q_stride + hk * K;
+    const E *dop = static_cast<const E *>(p.v) + (long long)sq.begin * row + hv * p.V + value0;
+    E *dvp = static_cast<E *>(p.out) + (long long)sq.begin * row + hv * p.V + value0;
+    E *drp = static_cast<E *>(p.mid) + (long long)sq.begin * row + hv * p.V + value0;
+    const size_t rec_step = (size_t)p.Hv * Rec::kBytes;
+    const char *rec = p.records + ((size_t)sq.slot0 * p.Hv + hv) * Rec::kBytes;
+    E *states = static_cast<E *>(p.states) +
+                ((size_t)sq.slot0 * p.Hv + hv) * state_size + (size_t)value0 * K;
+
+    auto live_of = [&](int c) {
+        const int left = c >= 0 ? len - c * kChunk : 0;
+        return left < kChunk ? left : kChunk;
+    };
+    auto buffer = [&](int c) { return lds + (c & 1) * kBuffer; };
+
+    Stage<E, K, kChunk, kThreads> gk, gq;
+    Stage<E, 16, kChunk, 64> go;  // this wave's values
+    float gs, last_next;
+    Split<E> T[6], P[6];
+    auto record = [&](int c) { return rec + (long long)c * (long long)rec_step; };
+    auto fetch_rows = [&](int c) {
+        const int live = live_of(c);
+        gk.load(kp + (long long)c * kChunk * p.k_stride, p.k_stride, live, tid);
+        gq.load(qp + (long long)c * kChunk * p.q_stride, p.q_stride, live, tid);
+        gs = Buffer(record(c) + Rec::kScalars, live > 0 ? kScalarSpace : 0).load_float(tid * 4);
+    };
+    auto put_rows = [&](int c) {
+        char *b = buffer(c);
+        gk.store(Tile<E, K>{reinterpret_cast<E *>(b)}, tid);
+        gq.store(Tile<E, K>{reinterpret_cast<E *>(b + kTile)}, tid);
+        reinterpret_cast<float *>(b + 2 * kTile)[tid] = gs;
+    };
+    auto fetch_values = [&](int c) {
+        go.load(dop + (long long)c * kChunk * row, row, live_of(c), lane);
+        last_next =
+            Buffer(record(c) + Rec::kScalars + kScalarSpace, c >= 0 ? 4 : 0).load_float(0);
+    };
+    auto fetch_T = [&](int c) {
+        const char *src = rec + (c > 0 ? c : 0) * rec_step;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    D.t[m][n] = mma(aq, bo[n], mma(ak, b[n], D.t[m][n]));
+        for (int f = 0; f < 6; ++f) T[f] = get_split<E>(src + f * Rec::kSplitBytes, lane);
+    };
+    auto fetch_P = [&](int c) {
+        const char *src = rec + (c > 0 ? c : 0) * rec_step + Rec::kP;
+#pragma unroll
+        for (int f = 0; f < 6; ++f) P[f] = get_split<E>(src + f * Rec::kSplitBytes, lane);
+    };
+    if (chunks > 0) {
+        fetch_rows(chunks - 1);
+        fetch_values(chunks - 1);
+        fetch_P(chunks - 1);
+        fetch_T(chunks - 1);
+        put_rows(chunks - 1);
+        fetch_rows(chunks - 2);
+    }
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int live = live_of(c);
+        __syncthreads();
+        put_rows(c - 1);
+        fetch_rows(c - 2);
+        char *b0 = buffer(c);
+        const Tile<E, K> tk{reinterpret_cast<E *>(b0)}, tq{reinterpret_cast<E *>(b0 + kTile)};
+        const Scalars &sc = *reinterpret_cast<const Scalars *>(b0 + 2 * kTile);  // without `last`
+        go.store(to, lane);
+        const float last = last_next;
+        const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)],
+                    beta = sc.beta[own_token(lane)];
+        fetch_values(c - 1);
+        store_rounded<E>(D, states + (size_t)c * p.Hv * state_size, g, lo);
+
+        // dU = diag(c_C / c) K D^T + P^T dO
+        f32x4 X[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) X[i] = zero();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const Split<E> b = to_split<E>(D.t[2 * ks], D.t[2 * ks + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                X[i] = mma(tk.rows(tile_row(i, lo), 32 * ks, g), b, X[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            X[i] *= row_bcast4(kD, i);
+        Frag<E> fo[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) fo[st] = to.template cols<4>(32 * st, 0, lane);
+#pragma unroll
+        for (int f = 0; f < 6; ++f) X[kUpTile[f]] = mma(P[f], fo[kUpStep[f]], X[kUpTile[f]]);
+        fetch_P(c - 1);
+        // dR = T^T dU
+        f32x4 R[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) R[i] = zero();
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const Split<E> b = to_split<E>(X[2 * st], X[2 * st + 1]);
+#pragma unroll
+            for (int f = 0; f < 6; ++f)
+                if (kUpStep[f] == st) R[kUpTile[f]] = mma(T[f], b, R[kUpTile[f]]);
+        }
+        fetch_T(c - 1);
+        {
+            const Buffer bv(dvp + (long long)c * kChunk * row, row_bytes<E>(live, row)),
+                br(drp + (long long)c * kChunk * row, row_bytes<E>(live, row));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t0 = tile_row(i, 4 * g);
+                const f32x4 be = row_bcast4(beta, i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned off = (unsigned)((t0 + e) * row + lo) * (unsigned)sizeof(E);
+                    br.store1(off, R[i][e], E());
+                    bv.store1(off, be[e] * R[i][e], E());
+                }
+                R[i] *= row_bcast4(kS, i);
+            }
+        }
+        // dS0 = c_C D + dO^T diag(scale c / |q|) Q - dR^T diag(beta c / |k|) K
+#pragma unroll
+        for (int m = 0; m < K / 16; ++m) D.t[m] *= last;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const Split<E> b = to_split<E>(R[2 * st], R[2 * st + 1]);
+            f32x4 x0 = *reinterpret_cast<const f32x4 *>(sc.qS + 32 * st + 8 * g),
+                  x1 = *reinterpret_cast<const f32x4 *>(sc.qS + 32 * st + 8 * g + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x0[e] *= fo[st].at(e);
+                x1[e] *= fo[st].at(4 + e);
+            }
+            const Split<E> bo = to_split<E>(x0, x1);
+#pragma unroll
+            for (int m = 0; m < K / 16; ++m) {
+                const int col = 32 * (m >> 1) + 4 * (m & 1);
+                D.t[m] = mma(tk.template cols<8>(32 * st, col, lane), b, D.t[m]);
+                D.t[m] = mma(tq.template cols<8>(32 * st, col, lane), bo, D.t[m]);
             }
         }
     }
     if (p.s_out) store_state(D, p.s_out + state_at, g, lo);
 }
 
-template <class E, int K, int NT, int W>
-hipError_t launch_forward_t(const ChainArgs &a, bool train, int n_seq, hipStream_t stream) {
-    constexpr int kLds = 2 * tile_bytes<E, K>(kChunk);
-    const auto fn = train ? forward_chain_kernel<E, K, NT, W, true>
-                          : forward_chain_kernel<E, K, NT, W, false>;
+// shared memory of a chain workgroup
+template <class E, int K>
+constexpr int chain_lds() {
+    return 2 * (2 * tile_bytes<E, K>(kChunk) + kScalarSpace) + tile_bytes<E, kValues>(kChunk);
+}
+
+template <class F>
+hipError_t launch(F fn, size_t blocks, int threads, int lds, const ChainArgs &a,
+                  hipStream_t stream) {
     const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    const size_t blocks = (size_t)n_seq * a.Hv * (a.V / (16 * NT * W));
-    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * W), kLds, stream, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), lds, stream, a);
     return hipGetLastError();
 }
 
-template <class E, int K, int NT, int W>
+template <class E, int K, int W>
+hipError_t launch_forward_t(const ChainArgs &a, bool train, int units, int n_seq,
+                            hipStream_t stream) {
+    constexpr int kLds = ForwardLds<E, K, W>::kBytes;
+    const int parts = a.V / (16 * W), step_parts = (K + 16 * W - 1) / (16 * W);
+    if (a.seg) {
+        hipError_t e = launch(forward_chain_kernel<E, K, W, kSummary>,
+                              (size_t)units * a.Hv * (parts + step_parts), 64 * W, kLds, a, stream);
+        if (e != hipSuccess) return e;
+        e = launch(combine_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / 64), kThreads,
+                   (sizeof(E) == 2 ? 2 : 1) * tile_bytes<E, K>(K), a, stream);
+        if (e != hipSuccess) return e;
+    }
+    return launch(train ? forward_chain_kernel<E, K, W, kTrain>
+                        : forward_chain_kernel<E, K, W, kInfer>,
+                  (size_t)units * a.Hv * parts, 64 * W, kLds, a, stream);
+}
+
+template <class E, int K>
 hipError_t launch_backward_t(const ChainArgs &a, int n_seq, hipStream_t stream) {
-    constexpr int kLds = 2 * tile_bytes<E, K>(kChunk) + tile_bytes<E, 16 * NT * W>(kChunk);
-    const auto fn = backward_chain_kernel<E, K, NT, W>;
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (e != hipSuccess) return e;
-    const size_t blocks = (size_t)n_seq * a.Hv * (a.V / (16 * NT * W));
-    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(64 * W), kLds, stream, a);
-    return hipGetLastError();
+    return launch(backward_chain_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / kValues),
+                  kThreads, chain_lds<E, K>(), a, stream);
 }
 
 ChainArgs chain_args(const Problem &p) {
     ChainArgs a{};
-    a.lay = Layout{p.cu, p.n_seq, p.T, p.total, p.slots};
+    a.lay = Layout{p.cu, p.n_seq, p.T, p.total};
     a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.v_stride = p.v_stride;
     a.Hk = p.Hk; a.Hv = p.Hv; a.V = p.V; a.pool = p.pool;
     a.slots_in = p.slots_in; a.slots_out = p.slots_out;
@@ -489,7 +771,27 @@ ChainArgs chain_args(const Problem &p) {
 
 }  // namespace
 
-int chain_values(const Problem &, bool) { return 64; }
+// Waves of a forward workgroup: eight where whole workgroups of 128 values come out
+// (two waves per SIMD share one copy of the chunk); float tiles leave room for four.
+bool wide(const Problem &p) { return p.bf16 && p.V % 128 == 0; }
+
+Segments plan_segments(const Problem &p) {
+    Segments s{};
+    s.units = p.n_seq;
+    const long long chains = (long long)p.n_seq * p.Hv * (p.V / (wide(p) ? 128 : 64));
+    const long long average = p.total / p.n_seq;
+    if (chains > 64 || average < kMinSegment * 2) return s;
+    long long n = 256 / chains;                     // segments of an average sequence
+    if (n > average / kMinSegment) n = average / kMinSegment;
+    if (n < 2) return s;
+    const long long len = (average + n - 1) / n;
+    s.seg = (int)((len + kChunk - 1) / kChunk * kChunk);
+    s.units = p.cu ? p.total / s.seg + p.n_seq : p.n_seq * ((p.T + s.seg - 1) / s.seg);
+    const size_t heads = (size_t)s.units * p.Hv;
+    s.state_bytes = heads * p.V * p.K * 4;
+    s.step_bytes = heads * p.K * p.K * 4;
+    return s;
+}
 
 hipError_t launch_forward(const ForwardArgs &f, hipStream_t stream) {
     const Problem &p = f.p;
@@ -500,12 +802,20 @@ hipError_t launch_forward(const ForwardArgs &f, hipStream_t stream) {
     a.records = f.records;
     a.s_in = f.s0; a.s_out = f.s_out;
     a.out = f.o; a.states = f.s_ckpt; a.mid = f.u;
+    const Segments s = plan_segments(p);
+    a.seg = s.seg;
+    a.seg_state = reinterpret_cast<float *>(f.segments);
+    a.seg_step = f.segments + s.state_bytes;
     const bool train = f.s_ckpt != nullptr;
-    if (p.bf16)
-        return p.K == 64 ? launch_forward_t<bf16_t, 64, 1, 4>(a, train, p.n_seq, stream)
-                         : launch_forward_t<bf16_t, 128, 1, 4>(a, train, p.n_seq, stream);
-    return p.K == 64 ? launch_forward_t<float, 64, 1, 4>(a, train, p.n_seq, stream)
-                     : launch_forward_t<float, 128, 1, 4>(a, train, p.n_seq, stream);
+    const int u = s.units, n = p.n_seq;
+    if (!p.bf16)
+        return p.K == 64 ? launch_forward_t<float, 64, 4>(a, train, u, n, stream)
+                         : launch_forward_t<float, 128, 4>(a, train, u, n, stream);
+    if (wide(p))
+        return p.K == 64 ? launch_forward_t<bf16_t, 64, 8>(a, train, u, n, stream)
+                         : launch_forward_t<bf16_t, 128, 8>(a, train, u, n, stream);
+    return p.K == 64 ? launch_forward_t<bf16_t, 64, 4>(a, train, u, n, stream)
+                     : launch_forward_t<bf16_t, 128, 4>(a, train, u, n, stream);
 }
 
 hipError_t launch_backward_chain(const BackwardArgs &b, hipStream_t stream) {
@@ -518,10 +828,10 @@ hipError_t launch_backward_chain(const BackwardArgs &b, hipStream_t stream) {
     a.s_in = b.ds_T; a.s_out = b.ds0;
     a.out = b.dv; a.states = b.ds; a.mid = b.dr;
     if (p.bf16)
-        return p.K == 64 ? launch_backward_t<bf16_t, 64, 1, 4>(a, p.n_seq, stream)
-                         : launch_backward_t<bf16_t, 128, 1, 4>(a, p.n_seq, stream);
-    return p.K == 64 ? launch_backward_t<float, 64, 1, 4>(a, p.n_seq, stream)
-                     : launch_backward_t<float, 128, 1, 4>(a, p.n_seq, stream);
+        return p.K == 64 ? launch_backward_t<bf16_t, 64>(a, p.n_seq, stream)
+                         : launch_backward_t<bf16_t, 128>(a, p.n_seq, stream);
+    return p.K == 64 ? launch_backward_t<float, 64>(a, p.n_seq, stream)
+                     : launch_backward_t<float, 128>(a, p.n_seq, stream);
 }
 
 }  // namespace gdr

@@ -16,27 +16,35 @@
 // a sum over a rectangle of pairs, in which nothing cancels (differences of row
 // and column sums of the same matrices would).
 //
-// One workgroup of four waves per chunk and key head; it goes through the value
+// One workgroup of sixteen waves per chunk and key head; it goes through the value
 // heads that share the key head and adds their dq and dk up in registers, so no
-// atomics are needed and the order of the sums is fixed.  Wave w owns tokens
-// 16w .. 16w + 15.  It forms dP and dA in both orientations (rows s for the
-// sums over s, rows t for those over t): each then is an operand of the next
-// product as it stands, which costs five products of 16 x 16 x V twice instead
-// of an exchange between waves.
+// atomics are needed and the order of the sums is fixed.  Wave (w, part) owns
+// tokens 16w .. 16w + 15 and a quarter of the keys.  Results over keys are kept as
+// [keys, tokens] tiles, so that a lane has one token and four neighbouring keys of
+// it: factors of the token are one register, and dq, dk leave in pieces of four.
+// Parts 0 and 1 form dP and dA with rows s, parts 2 and 3 with rows t (each
+// orientation is the operand of one of the products that follow), and pass them to
+// the others as operands through shared memory.  All tiles of the triangles are
+// formed, also those that are zero: branches around a few matrix products would
+// keep the compiler from having their operands in flight together, which costs more.
+//
+// What is read once per value head (U, dO, dR, S0, D) goes through two buffers in
+// steps of 64 values (float: one buffer, 32 values); the next step's pieces are on
+// their way to registers while one is multiplied.
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
 namespace gdr {
 namespace {
 
-constexpr int kVt = 32;                // values per step
 constexpr int kPitchM = kChunk + 4;
+constexpr int kThreads = 1024;
 
 struct GradArgs {
     Layout lay;
     const void *q, *k, *v, *g, *beta, *d_o, *s_ckpt, *u, *ds, *dr;
     void *dq, *dk, *dg, *dbeta;
-    long long q_stride, k_stride, v_stride;
+    int q_stride, k_stride, v_stride;
     int Hk, Hv, V;
     float scale;
     bool normalize;
@@ -46,345 +54,408 @@ __device__ __forceinline__ f32x4 zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
 template <class E, int K>
 struct GradLds {
-    static constexpr int kQ = tile_bytes<E, K>(kChunk);
-    static constexpr int kO = 2 * kQ;
-    static constexpr int kOSize = tile_bytes<E, kVt>(kChunk);
-    static constexpr int kS = kO + 3 * kOSize;
-    static constexpr int kSSize = tile_bytes<E, K>(kVt);
-    static constexpr int kBytes = kS + 2 * kSSize;
-    // M takes the place of the value steps' tiles
-    static_assert(3 * kOSize + 2 * kSSize >= kChunk * kPitchM * 4, "M fits");
+    static constexpr int kVt = 128 / (int)sizeof(E);  // values per step
+    static constexpr int kRows = tile_bytes<E, K>(kChunk);
+    static constexpr int kO = tile_bytes<E, kVt>(kChunk), kS = tile_bytes<E, K>(kVt);
+    static constexpr int kStep = 3 * kO + 2 * kS;
+    static constexpr int kBuffers = sizeof(E) == 2 ? 2 : 1;
+    // in the place of a head's last step: M, and the waves' 4 x 2 fragments
+    static constexpr int kM = kChunk * kPitchM * 4, kFrag = 512 * (int)sizeof(E);
+    static constexpr int kAfter = kM + 4 * 8 * kFrag;
+    static constexpr int kSpace = kAfter > kStep ? kAfter : kStep;
+    static constexpr int kBytes = 2 * kRows + kBuffers * kSpace;
+    static_assert(kBytes <= 156 * 1024, "fits a CU");
 };
 
-template <class E, int K>
-__global__ __launch_bounds__(256) void gradient_kernel(GradArgs p) {
-    using L = GradLds<E, K>;
-    constexpr int NK = K / 16;
-    extern __shared__ __align__(16) char lds[];
-    Tile<E, K> tk{reinterpret_cast<E *>(lds)}, tq{reinterpret_cast<E *>(lds + L::kQ)};
-    Tile<E, kVt> to{reinterpret_cast<E *>(lds + L::kO)},
-        tr{reinterpret_cast<E *>(lds + L::kO + L::kOSize)},
-        tu{reinterpret_cast<E *>(lds + L::kO + 2 * L::kOSize)};
-    Tile<E, K> ts{reinterpret_cast<E *>(lds + L::kS)},
-        td{reinterpret_cast<E *>(lds + L::kS + L::kSSize)};
-    float *sM = reinterpret_cast<float *>(lds + L::kO);
-    __shared__ double sG[kChunk];
-    __shared__ float sBeta[kChunk], sGrown[kChunk], sRest[kChunk], sRk[kChunk], sRq[kChunk];
-    __shared__ float sEntry[kChunk], sLeave[kChunk], sKS[kChunk], sDb[kChunk], sDRV[kChunk],
-        sPairs[kChunk], sDS[4];
+// product of two pieces of 16 bytes, element by element
+template <class E>
+__device__ __forceinline__ float dot_piece(u32x4 a, u32x4 b, float sum) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(E) == 2)
+            sum += wkv7::bf16_lo(a[i]) * wkv7::bf16_lo(b[i]) +
+                   wkv7::bf16_hi(a[i]) * wkv7::bf16_hi(b[i]);
+        else
+            sum += __uint_as_float(a[i]) * __uint_as_float(b[i]);
+    }
+    return sum;
+}
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
-    const int half = wave >> 1;
+// four neighbouring elements of a row
+template <class E, int C>
+__device__ __forceinline__ f32x4 row4(Tile<E, C> t, int row, int col) {
+    const E *s = t.p + t.offset(row, col);
+    if constexpr (sizeof(E) == 2) {
+        const u32x2 u = *reinterpret_cast<const u32x2 *>(s);
+        return f32x4{wkv7::bf16_lo(u[0]), wkv7::bf16_hi(u[0]), wkv7::bf16_lo(u[1]),
+                     wkv7::bf16_hi(u[1])};
+    } else {
+        return *reinterpret_cast<const f32x4 *>(s);
+    }
+}
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
+    return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+}
+
+// The same number, unknown to the compiler: addresses made from it are formed where
+// they are used instead of being kept in registers across the loops (there are
+// hundreds of them, and they would leave no room for the results).
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+template <class E, int K>
+__global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
+    using L = GradLds<E, K>;
+    constexpr int kVt = L::kVt, NK = K / 64;  // tiles of 16 keys of this wave
+    extern __shared__ __align__(16) char lds[];
+    const Tile<E, K> tk{reinterpret_cast<E *>(lds)}, tq{reinterpret_cast<E *>(lds + L::kRows)};
+    __shared__ Sum2 sG[kChunk];
+    __shared__ __align__(16) float sBeta[kChunk], sRk[kChunk], sRq[kChunk];
+    __shared__ float sGrown[kChunk], sRest[kChunk];
+    __shared__ float sEntry[4][kChunk], sLeave[4][kChunk], sKS[4][kChunk], sDb[kChunk],
+        sDRV[kChunk], sPairs[kChunk], sDS[16];
+
+    int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, lo = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = wave & 3, part = wave >> 2;  // token tile, quarter of the keys
+    const int key0 = part * (K / 4);
+    int mine = 16 * w + lo;  // this lane's token
+    auto refresh = [&]() {
+        tid = fresh(tid);
+        lane = tid & 63;
+        g = lane >> 4;
+        lo = lane & 15;
+        mine = 16 * w + lo;
+    };
     const int slot = (int)(blockIdx.x / p.Hk), hk = (int)(blockIdx.x % p.Hk);
     Seq sq;
-    p.lay.find(slot, sq);
+    p.lay.find(slot, kChunk, sq);
     const int first = sq.begin + (slot - sq.slot0) * kChunk;
     if (slot < sq.slot0 || first >= sq.end) return;  // the whole workgroup
     const int live = sq.end - first < kChunk ? sq.end - first : kChunk;
-    const int rep = p.Hv / p.Hk;
-    const long long row = (long long)p.Hv * p.V;
+    const int rep = p.Hv / p.Hk, row = p.Hv * p.V;
+    const int steps = p.V / kVt;
 
+    // The pieces of a step: half of the threads have dO and U, the others dR and v
+    // (for their product only); those of S0 and D go to as many as there are.
+    constexpr int kStateThreads = L::kS / 16 < kThreads ? L::kS / 16 : kThreads;
+    const bool upper = wave >= 8, with_states = wave < kStateThreads / 64;
+    Stage<E, kVt, kChunk, 512> ga, gb;
+    Stage<E, K, kVt, kStateThreads> gs, gd;
+    auto fetch = [&](int r, int v0) {
+        const int hv = hk * rep + r;
+        const int in = r < rep ? live : 0, rows = r < rep && with_states ? kVt : 0;
+        const size_t at = (size_t)first * row + hv * p.V + v0;
+        const size_t st = ((size_t)slot * p.Hv + hv) * p.V * K + (size_t)v0 * K;
+        ga.load(static_cast<const E *>(upper ? p.dr : p.d_o) + at, row, in, tid & 511);
+        gb.load(upper ? static_cast<const E *>(p.v) + (size_t)first * p.v_stride + hv * p.V + v0
+                      : static_cast<const E *>(p.u) + at,
+                upper ? p.v_stride : row, in, tid & 511);
+        gs.load(static_cast<const E *>(p.s_ckpt) + st, K, rows, tid);
+        gd.load(static_cast<const E *>(p.ds) + st, K, rows, tid);
+    };
     {
-        Stage<E, K, kChunk, 256> a, b;
-        a.load(static_cast<const E *>(p.k) + first * p.k_stride + (long long)hk * K, p.k_stride,
+        constexpr int kRowThreads = L::kRows / 16 < kThreads ? L::kRows / 16 : kThreads;
+        Stage<E, K, kChunk, kRowThreads> a, b;
+        a.load(static_cast<const E *>(p.k) + (long long)first * p.k_stride + hk * K, p.k_stride,
                live, tid);
-        b.load(static_cast<const E *>(p.q) + first * p.q_stride + (long long)hk * K, p.q_stride,
+        b.load(static_cast<const E *>(p.q) + (long long)first * p.q_stride + hk * K, p.q_stride,
                live, tid);
-        a.store(tk, tid);
-        b.store(tq, tid);
+        if (wave < kRowThreads / 64) {
+            a.store(tk, tid);
+            b.store(tq, tid);
+        }
     }
+    fetch(0, 0);
     __syncthreads();
-    {  // reciprocal norms: four lanes per token
-        const int t = tid >> 2, part = tid & 3;
-        float a = 0.f, b = 0.f;
-#pragma unroll 8
-        for (int c = part * (K / 4); c < (part + 1) * (K / 4); ++c) {
-            const float x = tk.at(t, c), y = tq.at(t, c);
-            a += x * x;
-            b += y * y;
-        }
-        a += wkv7::dpp_mov<wkv7::kDppQuadXor1>(a);
-        a += wkv7::dpp_mov<wkv7::kDppQuadXor2>(a);
-        b += wkv7::dpp_mov<wkv7::kDppQuadXor1>(b);
-        b += wkv7::dpp_mov<wkv7::kDppQuadXor2>(b);
-        if (part == 0) {
-            sRk[t] = p.normalize ? 1.f / sqrtf(a + kNormEps) : 1.f;
-            sRq[t] = p.normalize ? 1.f / sqrtf(b + kNormEps) : 1.f;
-        }
+    if (wave < 8) {  // 256 threads do k, 256 do q
+        const float a = reciprocal_norm(wave < 4 ? tk : tq, p.normalize, live, tid & 255);
+        if ((tid & 3) == 0) (wave < 4 ? sRk : sRq)[(tid & 255) >> 2] = a;
     }
-    // k.k and q.k, rows s in tile_row order, columns t = 16 wave + lo
-    f32x4 kk[4], qk[4];
+    // q.k (part 0) or k.k, rows s in tile_row order, columns t = 16 w + lo
+    f32x4 kq[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kk[i] = qk[i] = zero();
+    for (int i = 0; i < 4; ++i) kq[i] = zero();
+    if (part < 2)
 #pragma unroll
-    for (int ks = 0; ks < K / 32; ++ks) {
-        const Frag<E> bk = tk.rows(16 * wave + lo, 32 * ks, g),
-                      bq = tq.rows(16 * wave + lo, 32 * ks, g);
+        for (int ks = 0; ks < K / 32; ++ks) {
+            const Frag<E> b = (part ? tk : tq).rows(mine, 32 * ks, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < 2 * half + 2) {
-                const Frag<E> a = tk.rows(tile_row(i, lo), 32 * ks, g);
-                kk[i] = mma(a, bk, kk[i]);
-                qk[i] = mma(a, bq, qk[i]);
-            }
-    }
+            for (int i = 0; i < 4; ++i)
+                kq[i] = mma(tk.rows(tile_row(i, lo), 32 * ks, g), b, kq[i]);
+        }
+    // [keys key0 + 16 n + 4g + e, token 16 w + lo]
     f32x4 dQ[NK], dK[NK];
 #pragma unroll
     for (int n = 0; n < NK; ++n) dQ[n] = dK[n] = zero();
 
+    int buffer = 0;
     for (int r = 0; r < rep; ++r) {
         const int hv = hk * rep + r;
-        const size_t chunk_head = (size_t)slot * p.Hv + hv;
-        const E *op = static_cast<const E *>(p.d_o) + first * row + (long long)hv * p.V;
-        const E *rp = static_cast<const E *>(p.dr) + first * row + (long long)hv * p.V;
-        const E *up = static_cast<const E *>(p.u) + first * row + (long long)hv * p.V;
-        const E *sp = static_cast<const E *>(p.s_ckpt) + chunk_head * p.V * K;
-        const E *dp = static_cast<const E *>(p.ds) + chunk_head * p.V * K;
-        const E *vp = static_cast<const E *>(p.v) + first * p.v_stride + (long long)hv * p.V;
-
-        f32x4 oS[NK], rS[NK], uD[NK], P1[4], A1[4], P2[4], A2[4];
+        // parts 0, 1: dP^T, -dA^T, rows s; parts 2, 3: dP, -dA, rows t, columns s
+        f32x4 oS[NK], rS[NK], uD[NK], P[4];
 #pragma unroll
         for (int n = 0; n < NK; ++n) oS[n] = rS[n] = uD[n] = zero();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) P1[i] = A1[i] = P2[i] = A2[i] = zero();
+        for (int i = 0; i < 4; ++i) P[i] = zero();
         float ds_sum = 0.f, drv = 0.f;
-
-        for (int v0 = 0; v0 < p.V; v0 += kVt) {
-            Stage<E, kVt, kChunk, 256> go, gr, gu;
-            Stage<E, K, kVt, 256> gs, gd;
-            go.load(op + v0, row, live, tid);
-            gr.load(rp + v0, row, live, tid);
-            gu.load(up + v0, row, live, tid);
-            gs.load(sp + (size_t)v0 * K, K, kVt, tid);
-            gd.load(dp + (size_t)v0 * K, K, kVt, tid);
-            __syncthreads();  // the last step's reads (and those of the last head's M)
-            go.store(to, tid);
-            gr.store(tr, tid);
-            gu.store(tu, tid);
-            gs.store(ts, tid);
-            gd.store(td, tid);
+        float gt = 0.f, bt = 0.f;
+        const long long gate_at = (long long)(first + lane) * p.Hv + hv;
+        if (wave == 0 && lane < live) {
+            gt = to_float(static_cast<const E *>(p.g)[gate_at]);
+            bt = to_float(static_cast<const E *>(p.beta)[gate_at]);
+        }
+        char *b0 = lds;
+        for (int j = 0; j < steps; ++j) {
+            b0 = lds + 2 * L::kRows + (L::kBuffers == 2 ? buffer * L::kSpace : 0);
+            buffer ^= 1;
+            const Tile<E, kVt> to{reinterpret_cast<E *>(b0)}, tr{reinterpret_cast<E *>(b0 + L::kO)},
+                tu{reinterpret_cast<E *>(b0 + 2 * L::kO)};
+            const Tile<E, K> ts{reinterpret_cast<E *>(b0 + 3 * L::kO)},
+                td{reinterpret_cast<E *>(b0 + 3 * L::kO + L::kS)};
+            if (L::kBuffers == 1) __syncthreads();  // the buffer has been read
+            refresh();
+            ga.store(upper ? tr : to, tid & 511);
+            if (!upper) gb.store(tu, tid & 511);
+            if (with_states) {
+                gs.store(ts, tid);
+                gd.store(td, tid);
+            }
+            if (upper) drv = dot_piece<E>(ga.x[0], gb.x[0], drv);  // eight lanes per token
+#pragma unroll
+            for (int i = 0; i < gs.kPer; ++i) ds_sum = dot_piece<E>(gs.x[i], gd.x[i], ds_sum);
+            if (j + 1 < steps)
+                fetch(r, (j + 1) * kVt);
+            else
+                fetch(r + 1, 0);
             __syncthreads();
-            const Frag<E> fo = to.rows(16 * wave + lo, 0, g), fr = tr.rows(16 * wave + lo, 0, g),
-                          fu = tu.rows(16 * wave + lo, 0, g);
+            const Tile<E, kVt> ta = part < 2 ? tu : part == 2 ? to : tr,
+                               tb = part == 0 ? to : part == 1 ? tr : tu;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = tile_row(i, lo);
-                if (i < 2 * half + 2) {
-                    const Frag<E> a = tu.rows(t, 0, g);
-                    P1[i] = mma(a, fo, P1[i]);
-                    A1[i] = mma(a, fr, A1[i]);
+            for (int x = 0; x < kVt; x += 32) {
+                const Frag<E> fo = to.rows(mine, x, g), fr = tr.rows(mine, x, g),
+                              fu = tu.rows(mine, x, g), fb = tb.rows(mine, x, g);
+                Frag<E> as[NK], ad[NK], a[4];
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    as[n] = ts.template cols<4>(x, key0 + 16 * n, lane);
+                    ad[n] = td.template cols<4>(x, key0 + 16 * n, lane);
                 }
-                if (i >= 2 * half) {
-                    P2[i] = mma(to.rows(t, 0, g), fu, P2[i]);
-                    A2[i] = mma(tr.rows(t, 0, g), fu, A2[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = ta.rows(tile_row(i, lo), x, g);
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    oS[n] = mma(as[n], fo, oS[n]);
+                    rS[n] = mma(as[n], fr, rS[n]);
+                    uD[n] = mma(ad[n], fu, uD[n]);
                 }
-            }
 #pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                const Frag<E> bs = ts.template cols<4>(0, 16 * n, lane),
-                              bd = td.template cols<4>(0, 16 * n, lane);
-                oS[n] = mma(fo, bs, oS[n]);
-                rS[n] = mma(fr, bs, rS[n]);
-                uD[n] = mma(fu, bd, uD[n]);
-            }
-            {  // <D, S0>: 32 K products
-                const int x = tid >> 3, y0 = (tid & 7) * (K / 8);
-#pragma unroll 8
-                for (int y = y0; y < y0 + K / 8; ++y) ds_sum += ts.at(x, y) * td.at(x, y);
-            }
-            {  // dR . v: four lanes per token
-                const int t = tid >> 2, x0 = (tid & 3) * (kVt / 4);
-                if (t < live)
-#pragma unroll
-                    for (int x = x0; x < x0 + kVt / 4; ++x)
-                        drv += tr.at(t, x) * to_float(vp[t * p.v_stride + v0 + x]);
+                for (int i = 0; i < 4; ++i) P[i] = mma(a[i], fb, P[i]);
             }
         }
         if (wave == 0) {
-            const long long at = (long long)(first + lane) * p.Hv + hv;
-            const float gt = lane < live ? to_float(static_cast<const E *>(p.g)[at]) : 0.f;
-            const float bt = lane < live ? to_float(static_cast<const E *>(p.beta)[at]) : 0.f;
-            const double G = scan_decay(gt, lane);
+            const Sum2 G = scan_decay(gt);
             sG[lane] = G;
             sBeta[lane] = bt;
-            sGrown[lane] = decay(G, 0.0);
-            sRest[lane] = decay(__shfl(G, 63), G);
+            sGrown[lane] = decay(G);
+            sRest[lane] = decay(last_lane(G), G);
         }
-        drv += wkv7::dpp_mov<wkv7::kDppQuadXor1>(drv);
-        drv += wkv7::dpp_mov<wkv7::kDppQuadXor2>(drv);
-        if ((tid & 3) == 0) sDRV[tid >> 2] = drv;
+        if (upper) {
+            drv = wkv7::sum_lanes8(drv);
+            if ((tid & 7) == 0) sDRV[(tid & 511) >> 3] = drv;
+        }
         ds_sum = wkv7::sum_rows4(wkv7::sum_lanes16(ds_sum));
         if (lane == 0) sDS[wave] = ds_sum;
-        __syncthreads();
+        __syncthreads();  // also: the last step has been read
+        refresh();
+        float *sM = reinterpret_cast<float *>(b0);
+        char *frags = b0 + L::kM + w * (8 * L::kFrag);  // P^T, A^T, P, A of this token tile
+        const Sum2 Gm = sG[mine];
+        const float be = sBeta[mine], rk = sRk[mine], rq = sRq[mine];
 
-        // what goes through the states
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = 16 * wave + 4 * g + e;
-            const float grown = sGrown[t], rest = sRest[t], be = sBeta[t], rk = sRk[t],
-                        rq = sRq[t];
+        {  // what goes through the states; here the lane's token is t
+            const float grown = sGrown[mine], rest = sRest[mine], qf = p.scale * grown,
+                        kf = -be * grown;
             float oq = 0.f, rkd = 0.f, ud = 0.f;
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
-                const float kx = tk.at(t, 16 * n + lo), qx = tq.at(t, 16 * n + lo);
-                oq += oS[n][e] * qx;
-                rkd += rS[n][e] * kx;
-                ud += uD[n][e] * kx;
-                dQ[n][e] += p.scale * grown * oS[n][e];
-                dK[n][e] += rest * uD[n][e] - be * grown * rS[n][e];
+                const f32x4 k4 = row4(tk, mine, key0 + 16 * n + 4 * g),
+                            q4 = row4(tq, mine, key0 + 16 * n + 4 * g);
+                oq += dot4(oS[n], q4);
+                rkd += dot4(rS[n], k4);
+                ud += dot4(uD[n], k4);
+                dQ[n] += qf * oS[n];
+                dK[n] += rest * uD[n] + kf * rS[n];
             }
-            oq = wkv7::sum_lanes16(oq) * p.scale * grown * rq;
-            rkd = wkv7::sum_lanes16(rkd) * grown * rk;
-            ud = wkv7::sum_lanes16(ud) * rest * rk;
-            if (lo == 0) {
-                sEntry[t] = oq - be * rkd;
-                sLeave[t] = ud;
-                sKS[t] = rkd;
+            oq = wkv7::sum_rows4(oq) * qf * rq;
+            rkd = wkv7::sum_rows4(rkd) * grown * rk;
+            ud = wkv7::sum_rows4(ud) * rest * rk;
+            if (g == 0) {
+                sEntry[part][mine] = oq - be * rkd;
+                sLeave[part][mine] = ud;
+                sKS[part][mine] = rkd;
             }
         }
-        // pairs, columns t = 16 wave + lo: MP and MA as left operands with rows t
-        {
-            const int t = 16 * wave + lo;
-            const double Gt = sG[t];
-            const float be = sBeta[t], rkt = sRk[t], rqt = sRq[t];
+        // the triangles: P becomes this part's operand, kq the pairs' terms of dg
+        f32x4 pairs[4];
+        if (part < 2) {  // the lane's token is t, rows are s
             float db = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (i >= 2 * half + 2) break;
+                const f32x4 rks = *reinterpret_cast<const f32x4 *>(sRk + tile_row(i, 4 * g));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int s = tile_row(i, 4 * g + e);
-                    const float rks = sRk[s];
-                    const float E_ts = s <= t ? decay(Gt, sG[s]) : 0.f;
-                    const float mp = s <= t ? p.scale * E_ts * P1[i][e] : 0.f;
-                    const float da = s < t ? -E_ts * A1[i][e] : 0.f;
-                    const float dak = da * kk[i][e] * rkt * rks;
-                    db += dak;
-                    if (s < t) sM[t * kPitchM + s] = mp * qk[i][e] * rqt * rks + be * dak;
-                    P1[i][e] = mp * rks;
-                    A1[i][e] = be * da * rks;
+                    const int t = mine, s = tile_row(i, 4 * g + e);
+                    const float E_ts = decay(Gm, sG[s]);
+                    const float m = (part ? s < t : s <= t) ? E_ts * P[i][e] : 0.f;
+                    const float x = m * kq[i][e] * rks[e];
+                    db += x;
+                    pairs[i][e] = x;
+                    P[i][e] = m * rks[e];
                 }
+                const float f = part ? -be : p.scale, fx = f * (part ? rk : rq);
+                pairs[i] *= fx;
+                P[i] *= f;
             }
-            db = wkv7::sum_rows4(db);
-            if (g == 0) sDb[t] = db;
-        }
-        // and rows t, columns s = 16 wave + lo: the left operands MP^T and MA^T
-        {
-            const int s = 16 * wave + lo;
-            const double Gs = sG[s];
+            if (part) {
+                db = -rk * wkv7::sum_rows4(db);
+                if (g == 0) sDb[mine] = db;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<f32x4 *>(sM + mine * kPitchM + tile_row(i, 4 * g)) = pairs[i];
+            }
+        } else {  // the lane's token is s, rows are t
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (i < 2 * half) continue;
+                const int t0 = tile_row(i, 4 * g);
+                const f32x4 f = part == 2 ? p.scale * *reinterpret_cast<const f32x4 *>(sRq + t0)
+                                          : -(*reinterpret_cast<const f32x4 *>(sBeta + t0)) *
+                                                *reinterpret_cast<const f32x4 *>(sRk + t0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = tile_row(i, 4 * g + e);
-                    const float E_ts = s <= t ? decay(sG[t], Gs) : 0.f;
-                    P2[i][e] = s <= t ? p.scale * E_ts * P2[i][e] * sRq[t] : 0.f;
-                    A2[i][e] = s < t ? -sBeta[t] * E_ts * A2[i][e] * sRk[t] : 0.f;
+                    const int s = mine, t = t0 + e;
+                    const float E_ts = decay(sG[t], Gm);
+                    P[i][e] = (part == 2 ? s <= t : s < t) ? f[e] * E_ts * P[i][e] : 0.f;
                 }
             }
         }
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+            put_frag<E>(frags + (2 * part + st) * L::kFrag, to_frag<E>(P[2 * st], P[2 * st + 1]),
+                        lane);
+        __syncthreads();
+        refresh();
+        if (part == 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 *at = reinterpret_cast<f32x4 *>(sM + mine * kPitchM + tile_row(i, 4 * g));
+                *at += pairs[i];
+            }
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            if (st <= half) {
-                const Frag<E> fp = to_frag<E>(P1[2 * st], P1[2 * st + 1]),
-                              fa = to_frag<E>(A1[2 * st], A1[2 * st + 1]);
+            Frag<E> f[4], ak[NK], aq[NK];
 #pragma unroll
-                for (int n = 0; n < NK; ++n) {
-                    const Frag<E> b = tk.template cols<4>(32 * st, 16 * n, lane);
-                    dQ[n] = mma(fp, b, dQ[n]);
-                    dK[n] = mma(fa, b, dK[n]);
-                }
+            for (int x = 0; x < 4; ++x) f[x] = get_frag<E>(frags + (2 * x + st) * L::kFrag, lane);
+#pragma unroll
+            for (int n = 0; n < NK; ++n) {
+                ak[n] = tk.template cols<4>(32 * st, key0 + 16 * n, lane);
+                aq[n] = tq.template cols<4>(32 * st, key0 + 16 * n, lane);
             }
-            if (st >= half) {
-                const Frag<E> fp = to_frag<E>(P2[2 * st], P2[2 * st + 1]),
-                              fa = to_frag<E>(A2[2 * st], A2[2 * st + 1]);
 #pragma unroll
-                for (int n = 0; n < NK; ++n) {
-                    dK[n] = mma(fp, tq.template cols<4>(32 * st, 16 * n, lane), dK[n]);
-                    dK[n] = mma(fa, tk.template cols<4>(32 * st, 16 * n, lane), dK[n]);
-                }
+            for (int n = 0; n < NK; ++n) {
+                dQ[n] = mma(ak[n], f[0], dQ[n]);
+                dK[n] = mma(ak[n], f[1], dK[n]);
+                dK[n] = mma(aq[n], f[2], dK[n]);
+                dK[n] = mma(ak[n], f[3], dK[n]);
             }
         }
         __syncthreads();
-        // sums over the rectangles s < t <= t': down each quarter of a column first
+        // sums over the rectangles s < t <= t': down each sixteenth of a column first
         {
-            float run = 0.f;
             const int s = lane;
+            float x[4];
 #pragma unroll
-            for (int i = 15; i >= 0; --i) {
-                const int t = 16 * wave + i;
-                if (s < t) {
-                    run += sM[t * kPitchM + s];
-                    sM[t * kPitchM + s] = run;
-                }
+            for (int i = 0; i < 4; ++i) x[i] = sM[(4 * wave + i) * kPitchM + s];
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                x[i] = s < 4 * wave + i ? x[i] : 0.f;
+                if (i < 3) x[i] += x[i + 1];
+                sM[(4 * wave + i) * kPitchM + s] = x[i];
             }
         }
         __syncthreads();
-        {
-            const int t = tid >> 2, part = tid & 3, quarter = t >> 4;
-            float sum = 0.f;
+        {  // sixteen lanes per token; the sums above start at every fourth token
+            const int t = tid >> 4, c = tid & 15;
+            f32x4 sum = *reinterpret_cast<const f32x4 *>(sM + t * kPitchM + 4 * c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int s = 4 * i + part;
-                if (s < t) {
-                    sum += sM[t * kPitchM + s];
-                    for (int x = quarter + 1; x < 4; ++x) sum += sM[16 * x * kPitchM + s];
-                }
-            }
-            sum += wkv7::dpp_mov<wkv7::kDppQuadXor1>(sum);
-            sum += wkv7::dpp_mov<wkv7::kDppQuadXor2>(sum);
-            if (part == 0) sPairs[t] = sum;
+            for (int x = 1; x < 16; ++x)
+                if (4 * x > t)
+                    sum += *reinterpret_cast<const f32x4 *>(sM + 4 * x * kPitchM + 4 * c);
+            float one = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) one += 4 * c + e < t ? sum[e] : 0.f;
+            one = wkv7::sum_lanes16(one);
+            if (c == 0) sPairs[t] = one;
         }
         __syncthreads();
         if (wave == 0) {
-            float entry = sEntry[lane], leave = sLeave[lane];
-            const float own = leave;
+            float entry = 0.f, own = 0.f, ks = 0.f, whole = 0.f;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const float a = __shfl_down(entry, d), b = __shfl_up(leave, d);
-                if (lane + d < 64) entry += a;
-                if (lane >= d) leave += b;
+            for (int x = 0; x < 4; ++x) {
+                entry += sEntry[x][63 - lane];  // summed from the chunk's end
+                own += sLeave[x][lane];
+                ks += sKS[x][lane];
             }
-            const float whole = sGrown[63] * (sDS[0] + sDS[1] + sDS[2] + sDS[3]);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) whole += sDS[x];
+            sEntry[0][63 - lane] = scan_lanes(entry);
+            entry = sEntry[0][lane];
+            const float leave = scan_lanes(own);
+            whole *= sGrown[63];
             if (lane < live) {
-                const long long at = (long long)(first + lane) * p.Hv + hv;
-                static_cast<E *>(p.dg)[at] =
+                static_cast<E *>(p.dg)[gate_at] =
                     from_float<E>(sPairs[lane] + entry + (leave - own) + whole);
-                static_cast<E *>(p.dbeta)[at] =
-                    from_float<E>(sDRV[lane] - sKS[lane] + sDb[lane]);
+                static_cast<E *>(p.dbeta)[gate_at] = from_float<E>(sDRV[lane] - ks + sDb[lane]);
             }
         }
+        __syncthreads();  // before the next head's sums take their places
     }
 
     // the gradient of x / |x| from that of the unit vector, and out
-    E *dqp = static_cast<E *>(p.dq) + (long long)first * p.Hk * K + (long long)hk * K + lo;
-    E *dkp = static_cast<E *>(p.dk) + (long long)first * p.Hk * K + (long long)hk * K + lo;
+    if (p.normalize) {
+        const float rk = sRk[mine], rq = sRq[mine];
+        float a = 0.f, b = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int t = 16 * wave + 4 * g + e;
-        if (p.normalize) {
-            const float rk = sRk[t], rq = sRq[t];
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                a += dQ[n][e] * tq.at(t, 16 * n + lo);
-                b += dK[n][e] * tk.at(t, 16 * n + lo);
-            }
-            a = wkv7::sum_lanes16(a) * rq * rq;
-            b = wkv7::sum_lanes16(b) * rk * rk;
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                dQ[n][e] = rq * (dQ[n][e] - tq.at(t, 16 * n + lo) * a);
-                dK[n][e] = rk * (dK[n][e] - tk.at(t, 16 * n + lo) * b);
-            }
+        for (int n = 0; n < NK; ++n) {
+            a += dot4(dQ[n], row4(tq, mine, key0 + 16 * n + 4 * g));
+            b += dot4(dK[n], row4(tk, mine, key0 + 16 * n + 4 * g));
         }
-        if (t < live)
+        a = wkv7::sum_rows4(a);
+        b = wkv7::sum_rows4(b);
+        if (g == 0) {
+            sEntry[part][mine] = a;
+            sLeave[part][mine] = b;
+        }
+        __syncthreads();
+        a = (sEntry[0][mine] + sEntry[1][mine] + sEntry[2][mine] + sEntry[3][mine]) * rq * rq;
+        b = (sLeave[0][mine] + sLeave[1][mine] + sLeave[2][mine] + sLeave[3][mine]) * rk * rk;
 #pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                dqp[(long long)t * p.Hk * K + 16 * n] = from_float<E>(dQ[n][e]);
-                dkp[(long long)t * p.Hk * K + 16 * n] = from_float<E>(dK[n][e]);
-            }
+        for (int n = 0; n < NK; ++n) {
+            dQ[n] = rq * (dQ[n] - a * row4(tq, mine, key0 + 16 * n + 4 * g));
+            dK[n] = rk * (dK[n] - b * row4(tk, mine, key0 + 16 * n + 4 * g));
+        }
+    }
+    const int krow = p.Hk * K;
+    const Buffer bq(static_cast<E *>(p.dq) + (size_t)first * krow + hk * K, row_bytes<E>(live, krow)),
+        bk(static_cast<E *>(p.dk) + (size_t)first * krow + hk * K, row_bytes<E>(live, krow));
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+        const unsigned off = (unsigned)(mine * krow + key0 + 16 * n + 4 * g) * (unsigned)sizeof(E);
+        bq.store4(off, dQ[n], E());
+        bk.store4(off, dK[n], E());
     }
 }
 
@@ -395,7 +466,7 @@ hipError_t launch_gradients_t(const GradArgs &a, int slots, hipStream_t stream) 
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((size_t)slots * a.Hk)), dim3(256), kLds, stream, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)((size_t)slots * a.Hk)), dim3(kThreads), kLds, stream, a);
     return hipGetLastError();
 }
 
@@ -405,7 +476,7 @@ hipError_t launch_gradients(const BackwardArgs &b, hipStream_t stream) {
     const Problem &p = b.p;
     if (p.slots == 0) return hipSuccess;
     GradArgs a{};
-    a.lay = Layout{p.cu, p.n_seq, p.T, p.total, p.slots};
+    a.lay = Layout{p.cu, p.n_seq, p.T, p.total};
     a.q = b.q; a.k = b.k; a.v = b.v; a.g = b.g; a.beta = b.beta;
     a.d_o = b.d_o; a.s_ckpt = b.s_ckpt; a.u = b.u; a.ds = b.ds; a.dr = b.dr;
     a.dq = b.dq; a.dk = b.dk; a.dg = b.dg; a.dbeta = b.dbeta;

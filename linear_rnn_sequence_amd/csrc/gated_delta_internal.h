@@ -15,7 +15,7 @@ struct Problem {
     const int *cu;  // nullptr: dense
     int n_seq, T, total, slots;
     int Hk, Hv, K, V;
-    long long q_stride, k_stride, v_stride;  // elements from token to token
+    int q_stride, k_stride, v_stride;  // elements from token to token, at most 2^23
     const int *slots_in, *slots_out;
     int pool;
     float scale;
@@ -30,6 +30,7 @@ struct ForwardArgs {
     float *s_out;
     void *s_ckpt, *u;  // training: nullptr otherwise
     char *records;     // workspace
+    char *segments;    // workspace: the segments' states and transitions
 };
 
 struct BackwardArgs {
@@ -50,10 +51,17 @@ struct DecodeArgs {
     void *o;
 };
 
+// How the forward splits the sequences: segments of `seg` tokens (0: none), `units`
+// of them at most, and the bytes of their states and transitions.
+struct Segments {
+    int seg, units;
+    size_t state_bytes, step_bytes;
+};
+constexpr int kMinSegment = 512;  // tokens
+Segments plan_segments(const Problem &p);
+
 size_t forward_record_bytes(bool bf16);
 size_t backward_record_bytes(bool bf16);
-// values of one chain workgroup
-int chain_values(const Problem &p, bool backward);
 
 hipError_t launch_prep(const Problem &p, const void *q, const void *k, const void *g,
                        const void *beta, char *records, bool backward, hipStream_t stream);

@@ -28,7 +28,7 @@ struct PrepArgs {
     Layout lay;
     const void *q, *k, *g, *beta;
     char *records;
-    long long q_stride, k_stride;
+    int q_stride, k_stride;
     int Hk, Hv;
     float scale;
     bool normalize;
@@ -44,57 +44,61 @@ __device__ __forceinline__ f32x4 mul_block(const float *m, int row0, int col0, f
     return c;
 }
 
+template <class E, int K>
+constexpr int prep_lds() {
+    // A and T take the place of the k and q rows once their products are formed
+    constexpr int rows = 2 * tile_bytes<E, K>(kChunk), mats = 2 * kChunk * kPitchA * 4;
+    return rows > mats ? rows : mats;
+}
+
 template <class E, int K, bool BWD>
-__global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
+__global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
     using Rec = typename std::conditional<BWD, BwdRecord<E>, FwdRecord<E>>::type;
     extern __shared__ __align__(16) char lds[];
     Tile<E, K> tk{reinterpret_cast<E *>(lds)};
     Tile<E, K> tq{reinterpret_cast<E *>(lds + tile_bytes<E, K>(kChunk))};
-    float *sA = reinterpret_cast<float *>(lds + 2 * tile_bytes<E, K>(kChunk));
+    float *sA = reinterpret_cast<float *>(lds);
     float *sT = sA + kChunk * kPitchA;
-    __shared__ double sG[kChunk];
-    __shared__ float sBeta[kChunk], sRk[kChunk], sRq[kChunk];
+    constexpr int kHeads = 4;  // value heads whose decays are summed at a time
+    __shared__ Sum2 sG4[kHeads][kChunk];
+    __shared__ __align__(16) float sBeta4[kHeads][kChunk];
+    __shared__ float sRk[kChunk], sRq[kChunk];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63,
+              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
     const int slot = (int)(blockIdx.x / p.Hk), hk = (int)(blockIdx.x % p.Hk);
     Seq sq;
-    p.lay.find(slot, sq);
+    p.lay.find(slot, kChunk, sq);
     const int first = sq.begin + (slot - sq.slot0) * kChunk;
     if (slot < sq.slot0 || first >= sq.end) return;  // the whole workgroup
     const int live = sq.end - first < kChunk ? sq.end - first : kChunk;
     const int rep = p.Hv / p.Hk;
 
+    // the first four value heads' gates, wave by wave
+    float gate = 0.f, strength = 0.f;
+    auto load_gates = [&](int r) {
+        const size_t at = ((size_t)first + lane) * p.Hv + hk * rep + r;
+        const bool in = r < rep && lane < live;
+        gate = in ? to_float(static_cast<const E *>(p.g)[at]) : 0.f;
+        strength = in ? to_float(static_cast<const E *>(p.beta)[at]) : 0.f;
+    };
+    load_gates(wave);
     {
         Stage<E, K, kChunk, 256> sk, sqv;
-        sk.load(static_cast<const E *>(p.k) + first * p.k_stride + (long long)hk * K, p.k_stride,
+        sk.load(static_cast<const E *>(p.k) + (long long)first * p.k_stride + hk * K, p.k_stride,
                 live, tid);
-        sqv.load(static_cast<const E *>(p.q) + first * p.q_stride + (long long)hk * K, p.q_stride,
+        sqv.load(static_cast<const E *>(p.q) + (long long)first * p.q_stride + hk * K, p.q_stride,
                  live, tid);
         sk.store(tk, tid);
         sqv.store(tq, tid);
     }
-    // blocks above the diagonal of A and T that are read: zeros, once
-    for (int i = tid; i < kChunk * kPitchA; i += 256) {
-        sA[i] = 0.f;
-        sT[i] = 0.f;
-    }
     __syncthreads();
-    {  // reciprocal norms: four lanes per token
-        const int row = tid >> 2, part = tid & 3;
-        float a = 0.f, b = 0.f;
-#pragma unroll 8
-        for (int c = part * (K / 4); c < (part + 1) * (K / 4); ++c) {
-            const float x = tk.at(row, c), y = tq.at(row, c);
-            a += x * x;
-            b += y * y;
-        }
-        a += wkv7::dpp_mov<wkv7::kDppQuadXor1>(a);
-        a += wkv7::dpp_mov<wkv7::kDppQuadXor2>(a);
-        b += wkv7::dpp_mov<wkv7::kDppQuadXor1>(b);
-        b += wkv7::dpp_mov<wkv7::kDppQuadXor2>(b);
-        if (part == 0) {
-            sRk[row] = p.normalize ? 1.f / sqrtf(a + kNormEps) : 1.f;
-            sRq[row] = p.normalize ? 1.f / sqrtf(b + kNormEps) : 1.f;
+    {
+        const float a = reciprocal_norm(tk, p.normalize, live, tid);
+        const float b = reciprocal_norm(tq, p.normalize, live, tid);
+        if ((tid & 3) == 0) {
+            sRk[tid >> 2] = a;
+            sRq[tid >> 2] = b;
         }
     }
     // k.k: rows 16 wave + 4g + e, columns 16 j + lo, j <= wave (natural order)
@@ -127,46 +131,63 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
                 qk[n][h] = mma(ta.rows(tile_row(2 * step + h, lo), 32 * ks, g), b, qk[n][h]);
         }
     }
+    __syncthreads();
+    // blocks (0, 1) and (2, 3) of T: read as zeros, never written
+    if (tid < 128) {
+        const int row = 32 * (tid >> 6) + (tid & 15), col = row / 32 * 32 + 16 + 4 * (tid >> 4 & 3);
+        *reinterpret_cast<f32x4 *>(sT + row * kPitchA + col) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     for (int r = 0; r < rep; ++r) {
         const int hv = hk * rep + r;
         char *rec = p.records + ((size_t)slot * p.Hv + hv) * Rec::kBytes;
-        __syncthreads();  // the norms; the last head's reads of sA, sT, sG, sBeta
-        if (wave == 0) {
-            const long long at = (long long)(first + lane) * p.Hv + hv;
-            const float gt = lane < live ? to_float(static_cast<const E *>(p.g)[at]) : 0.f;
-            const float bt = lane < live ? to_float(static_cast<const E *>(p.beta)[at]) : 0.f;
-            const double G = scan_decay(gt, lane);
-            const double last = __shfl(G, 63);
-            sG[lane] = G;
-            sBeta[lane] = bt;
-            Scalars *sc = reinterpret_cast<Scalars *>(rec + Rec::kScalars);
-            const float from0 = decay(G, 0.0);
-            sc->beta[lane] = bt;
-            sc->kS[lane] = bt * from0 * sRk[lane];
-            sc->kD[lane] = decay(last, G) * sRk[lane];
-            sc->qS[lane] = p.scale * from0 * sRq[lane];
-            if (lane == 63) sc->last = from0;
+        if (r % kHeads == 0) {
+            if (r) __syncthreads();  // the last heads' reads of sG4, sBeta4
+            if (r) load_gates(r + wave);
+            if (r + wave < rep) {
+                const Sum2 G = scan_decay(gate);
+                sG4[wave][lane] = G;
+                sBeta4[wave][lane] = strength;
+                Scalars *sc = reinterpret_cast<Scalars *>(rec + wave * Rec::kBytes + Rec::kScalars);
+                const float from0 = decay(G);
+                sc->beta[lane] = strength;
+                sc->kS[lane] = -(BWD ? strength : 1.f) * from0 * sRk[lane];
+                sc->kD[lane] = decay(last_lane(G), G) * sRk[lane];
+                sc->qS[lane] = p.scale * from0 * sRq[lane];
+                if (lane == 63) sc->last = from0;
+            }
         }
-        __syncthreads();
+        __syncthreads();  // the above; the last head's reads of sA, sT
+        const Sum2 *sG = sG4[r % kHeads];
+        const float *sBeta = sBeta4[r % kHeads];
         f32x4 nd{0.f, 0.f, 0.f, 0.f}, ndt{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > wave) break;
-            const int col = 16 * j + lo;
-            const double Gc = sG[col];
-            const float rc = sRk[col], bc = sBeta[col];
+        {
+            Sum2 Gr[4];
+            float rr[4], br[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int row = 16 * wave + 4 * g + e;
-                const float x = kk[j][e] * sRk[row] * rc;
-                const float a =
-                    row > col ? sBeta[row] * decay(sG[row], Gc) * x : 0.f;
-                if (j < wave) {
-                    sA[row * kPitchA + col] = a;
-                } else {
-                    nd[e] = a;
-                    ndt[e] = col > row ? bc * decay(Gc, sG[row]) * x : 0.f;
+                Gr[e] = sG[row];
+                rr[e] = sRk[row];
+                br[e] = sBeta[row];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j > wave) break;
+                const int col = 16 * j + lo;
+                const Sum2 Gc = sG[col];
+                const float rc = sRk[col], bc = sBeta[col];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 16 * wave + 4 * g + e;
+                    const float x = kk[j][e] * rr[e] * rc;
+                    if (j < wave) {
+                        sA[row * kPitchA + col] = br[e] * decay(Gr[e], Gc) * x;
+                    } else {  // the diagonal block and its transpose stay in registers
+                        const float d = row > col ? decay(Gr[e], Gc) : decay(Gc, Gr[e]);
+                        nd[e] = row > col ? br[e] * d * x : 0.f;
+                        ndt[e] = row < col ? bc * d * x : 0.f;
+                    }
                 }
             }
         }
@@ -197,22 +218,27 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
                 }
             }
         }
-        // P needs nothing of T: formed while other waves finish their columns
+        // P needs nothing of T: formed while other waves finish their columns.  The
+        // waves with the fewest blocks above take two fragments each.
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const int f = wave + 4 * n;
             if (f >= 6) break;
             const int tile = BWD ? kUpTile[f] : kLowTile[f], step = BWD ? kUpStep[f] : kLowStep[f];
             const int col = tile_row(tile, lo);
+            const Sum2 Gc = sG[col];
+            const float rc = p.scale * (BWD ? sRk[col] : sRq[col]);
             f32x4 v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int row = tile_row(2 * step + h, 4 * g + e);
-                    const int t = BWD ? row : col, s = BWD ? col : row;
-                    v[h][e] = s <= t ? p.scale * sRq[t] * sRk[s] * decay(sG[t], sG[s]) * qk[n][h][e]
-                                     : 0.f;
+                    const bool in = BWD ? col <= row : row <= col;  // s <= t
+                    const Sum2 Gr = sG[row];
+                    const float w = rc * (BWD ? sRq[row] : sRk[row]) *
+                                    (BWD ? decay(Gr, Gc) : decay(Gc, Gr));
+                    v[h][e] = in ? w * qk[n][h][e] : 0.f;
                 }
             if constexpr (BWD)
                 put_split<E>(rec + Rec::kP + f * Rec::kSplitBytes, to_split<E>(v[0], v[1]), lane);
@@ -231,9 +257,12 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = sT[(t0 + j) * kPitchA + s];
             } else {
-                const float *src = sT + tile_row(kLowTile[f], lo) * kPitchA + 32 * kLowStep[f] + 8 * g;
-                v[0] = *reinterpret_cast<const f32x4 *>(src);
-                v[1] = *reinterpret_cast<const f32x4 *>(src + 4);
+                const int s0 = 32 * kLowStep[f] + 8 * g;
+                const float *src = sT + tile_row(kLowTile[f], lo) * kPitchA + s0;
+                v[0] = *reinterpret_cast<const f32x4 *>(src) *
+                       *reinterpret_cast<const f32x4 *>(sBeta + s0);
+                v[1] = *reinterpret_cast<const f32x4 *>(src + 4) *
+                       *reinterpret_cast<const f32x4 *>(sBeta + s0 + 4);
             }
             put_split<E>(rec + f * Rec::kSplitBytes, to_split<E>(v[0], v[1]), lane);
         }
@@ -242,7 +271,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs p) {
 
 template <class E, int K, bool BWD>
 hipError_t launch_prep_t(const PrepArgs &a, int slots, hipStream_t stream) {
-    constexpr int kLds = 2 * tile_bytes<E, K>(kChunk) + 2 * kChunk * kPitchA * 4;
+    constexpr int kLds = prep_lds<E, K>();
     const auto fn = prep_kernel<E, K, BWD>;
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -263,7 +292,7 @@ size_t backward_record_bytes(bool bf16) {
 hipError_t launch_prep(const Problem &p, const void *q, const void *k, const void *g,
                        const void *beta, char *records, bool backward, hipStream_t stream) {
     PrepArgs a{};
-    a.lay = Layout{p.cu, p.n_seq, p.T, p.total, p.slots};
+    a.lay = Layout{p.cu, p.n_seq, p.T, p.total};
     a.q = q; a.k = k; a.g = g; a.beta = beta;
     a.records = records;
     a.q_stride = p.q_stride; a.k_stride = p.k_stride;

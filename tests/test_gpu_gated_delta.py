@@ -495,3 +495,34 @@ def test_results_do_not_depend_on_the_batch_or_the_run(rnn):
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     alone = step([t[2:3].contiguous() for t in x.values()], d_o[2:3].contiguous())
     assert all(torch.equal(p[2:3], q) for p, q in zip(a, alone))
+
+
+@pytest.mark.parametrize("layout", [("bf16", 64, 64, 1, 2), ("bf16", 64, 128, 2, 2), ("bf16", 128, 128, 1, 2),
+                                    ("bf16", 128, 64, 1, 1), ("bf16", 128, 256, 1, 1), ("f32", 64, 64, 1, 2),
+                                    ("f32", 128, 256, 1, 1), ("f32", 128, 128, 2, 2)], ids=str)
+def test_long_sequences_of_few_heads(rnn, layout):
+    """Sequences long enough to be done in parallel segments, in place, next to short ones, against
+    the same tokens in pieces that are too short for it (the state carried in float32)."""
+    dtype, K, V, Hk, Hv = layout
+    lens = [3000, 1100, 0, 1500, 5]
+    x = inputs(sum(lens), Hk, Hv, K, V, dtype, 33, slow=True)
+    x["g"] *= 0.05                                      # far memories
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    pool = states(5, Hv, V, K, 3)
+    old = pool.clone()
+    need = rnn.gated_delta_forward_workspace_bytes
+    # the segments' states and transitions need workspace besides that of the chunks
+    assert need(sum(lens), Hk, Hv, K, V, sequences=5, packed=True, dtype=dtype) > \
+        need(64, 1, 1, K, V, dtype=dtype) * Hv * (sum(lens) // 64 + 5)
+    o, s = rnn.gated_delta_forward(*x.values(), s0=pool, s_out=pool, cu_seqlens=cu, normalize=True)
+    ot, st, ck, u = rnn.gated_delta_forward_train(*x.values(), s0=old, cu_seqlens=cu, normalize=True)
+    assert torch.equal(o, ot) and torch.equal(s, st)
+    for i, n in enumerate(lens):
+        a, S, parts = int(cu[i]), old[i:i + 1].clone(), []
+        for b in range(a, a + n, 400):
+            piece = [t[:, b:min(b + 400, a + n)].contiguous() for t in x.values()]
+            one, S = rnn.gated_delta_forward(*piece, s0=S, normalize=True)
+            parts.append(one)
+        close_state(pool[i], f64(S[0]), dtype)
+        if n:
+            close(o[:, a:a + n], f64(torch.cat(parts, 1)), dtype, f"o of sequence {i}")
