@@ -118,24 +118,39 @@ __device__ __forceinline__ Place place_of(unsigned block, int Hk, int Hv, int pa
     return at;
 }
 
+enum Mode { kInfer, kTrain, kSummary };
+
 // Shared memory of a forward workgroup of W waves: two buffers with a chunk's k and q
 // rows and its record (bf16) or the record's scalars (float), and each wave's
-// values.
-template <class E, int K, int W>
+// values.  kSummary has no use for q and P.  In bf16 with 128 keys and eight waves that
+// leaves 80 KB of 128, so that a CU has two workgroups, which take turns at waiting: 448
+// of them took 328 us, and 367 us one at a time.
+template <class E, int K, int W, Mode MODE>
 struct ForwardLds {
     static constexpr int kThreads = 64 * W;
     static constexpr int kTile = tile_bytes<E, K>(kChunk);
     static constexpr bool kRecord = sizeof(E) == 2;
-    static constexpr int kRecPer = (FwdRecord<E>::kBytes + 16 * kThreads - 1) / (16 * kThreads);
+    // a record's bytes behind those left out, and where its parts lie in shared memory
+    static constexpr int kPBytes = MODE == kSummary ? FwdRecord<E>::kScalars - FwdRecord<E>::kP : 0;
+    static constexpr int kScalarsAt = FwdRecord<E>::kScalars - kPBytes;
+    static constexpr int kRecPer =
+        (FwdRecord<E>::kBytes - kPBytes + 16 * kThreads - 1) / (16 * kThreads);
+    static constexpr int kRows = MODE == kSummary ? kTile : 2 * kTile;
     static constexpr int kRest = kRecord ? kRecPer * 16 * kThreads : kScalarSpace;
-    static constexpr int kBuffer = 2 * kTile + kRest;
-    static constexpr int kValueTile = tile_bytes<E, 16>(kChunk);
-    static constexpr int kBytes = 2 * kBuffer + W * kValueTile;
+    static constexpr int kBuffer = kRows + kRest;
+    // Values of a chunk: each wave's own, or the workgroup's rows of them, double-buffered,
+    // with o in their place afterwards.  The rows make whole lines of memory where a
+    // wave's 16 values are pieces of 32 bytes, but pass through shared memory twice more:
+    // with 64 keys, where memory is what a chunk waits for, 320 workgroups took
+    // 345 us with them and 375 us without; with 128 keys, where shared memory is the
+    // busier, 256 took 307 us with them and 278 us without.  float has no room.
+    static constexpr bool kShared = kRecord && MODE != kSummary && K == 64;
+    static constexpr int kValueCols = kShared ? 16 * W : 16;
+    static constexpr int kValueTile = tile_bytes<E, kValueCols>(kChunk);
+    static constexpr int kBytes = 2 * kBuffer + (kShared ? 2 : W) * kValueTile;
     static_assert(kBytes <= 160 * 1024, "fits a CU");
     static_assert(kRecord || kThreads == 256, "a float of each thread");
 };
-
-enum Mode { kInfer, kTrain, kSummary };
 
 // The chunks' shared rows are double-buffered in shared memory: while the waves work
 // on chunk c, the rows of c + 1 go from registers to the other buffer and those
@@ -156,9 +171,12 @@ template <class E, int K, int W, Mode MODE>
 __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_kernel(
     ChainArgs p) {
     using Rec = FwdRecord<E>;
-    using L = ForwardLds<E, K, W>;
+    using L = ForwardLds<E, K, W, MODE>;
     constexpr int KS = K / 32, kTile = L::kTile, kBuffer = L::kBuffer, kThreads = 64 * W;
-    constexpr int kValues = 16 * W, NT = 1;
+    constexpr int kValues = 16 * W;
+    // stores of an iteration behind its loads: the state (kTrain), u, and float's o
+    constexpr int kStores = (MODE == kTrain ? (K / 32 + 2) * (int)sizeof(E) / 2 : 0) +
+                            (L::kShared || MODE == kSummary ? 0 : 4);
     extern __shared__ __align__(16) char lds[];
 
     const int tid = threadIdx.x, lane = tid & 63,
@@ -168,7 +186,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
                               v_parts + (MODE == kSummary ? (K + kValues - 1) / kValues : 0));
     const int hv = at.hv, hk = hv / (p.Hv / p.Hk);
     const bool step = MODE == kSummary && at.part >= v_parts;  // a part of the transition
-    const int value0 = (step ? at.part - v_parts : at.part) * kValues + wave * 16 * NT;
+    const int value0 = (step ? at.part - v_parts : at.part) * kValues + wave * 16;
     const size_t state_size = (size_t)p.V * K;
 
     // the sequence, and this workgroup's chunks c0 .. c0 + chunks - 1 of it
@@ -194,7 +212,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
     // The start: of a sequence (kept in the place of its last segment's summary, which
     // nothing needs, since s_out may be s_in: the last segment may be done before
     // the first one starts), of a later segment, or zeros.
-    State<K> S[NT];
+    State<K> S;
     const float *from = nullptr;
     if (MODE != kSummary && !last_part && !first)
         from = p.seg_state + ((size_t)seg_last * p.Hv + hv) * state_size;
@@ -204,47 +222,49 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         const int in = slot_of(p.slots_in, seq, p.pool);
         if (in >= 0) from = p.s_in + ((size_t)in * p.Hv + hv) * state_size;
     }
+    if (from) {
+        load_state(S, from + (size_t)value0 * K, g, lo);
+    } else {
+        clear(S);
+        if (step)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (from) {
-            load_state(S[n], from + (size_t)(value0 + 16 * n) * K, g, lo);
-        } else {
-            clear(S[n]);
-            if (step)
+            for (int m = 0; m < K / 16; ++m)
 #pragma unroll
-                for (int m = 0; m < K / 16; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[n].t[m][e] = tile_row(m, 4 * g + e) == value0 + 16 * n + lo ? 1.f : 0.f;
-        }
+                for (int e = 0; e < 4; ++e)
+                    S.t[m][e] = tile_row(m, 4 * g + e) == value0 + lo ? 1.f : 0.f;
     }
 
     if (MODE == kSummary && !first)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            store_state(S[n], p.seg_state + ((size_t)seg_last * p.Hv + hv) * state_size +
-                                  (size_t)(value0 + 16 * n) * K, g, lo);
+        store_state(S, p.seg_state + ((size_t)seg_last * p.Hv + hv) * state_size +
+                           (size_t)value0 * K, g, lo);
 
     const E *kp = static_cast<const E *>(p.k) + token * p.k_stride + hk * K;
     const E *qp = static_cast<const E *>(p.q) + token * p.q_stride + hk * K;
-    const E *vp = static_cast<const E *>(p.v) + token * p.v_stride + hv * p.V + (step ? 0 : value0);
+    const int vcol = L::kShared ? wave * 16 : 0;  // this wave's values in the tile of them
+    const E *vp = static_cast<const E *>(p.v) + token * p.v_stride + hv * p.V +
+                  (step ? 0 : value0 - vcol);
     const int row = p.Hv * p.V;  // dense rows of o and u
-    E *op = static_cast<E *>(p.out) + token * row + hv * p.V + value0;
+    E *op = static_cast<E *>(p.out) + token * row + hv * p.V + value0 - vcol;
     E *up = static_cast<E *>(p.mid) + token * row + hv * p.V + value0;
     const size_t rec_step = (size_t)p.Hv * Rec::kBytes;
     const char *rec = p.records + ((size_t)(sq.slot0 + c0) * p.Hv + hv) * Rec::kBytes;
     E *states = static_cast<E *>(p.states) +
                 ((size_t)(sq.slot0 + c0) * p.Hv + hv) * state_size + (size_t)value0 * K;
-    const Tile<E, 16 * NT> tv{reinterpret_cast<E *>(lds + 2 * kBuffer + wave * L::kValueTile)};
+    using Values = Tile<E, L::kValueCols>;
 
     auto live_of = [&](int c) {
         const int left = len - c * kChunk;
         return left < kChunk ? left : kChunk;  // none or fewer: nothing is in range
     };
     auto buffer = [&](int c) { return lds + (c & 1) * kBuffer; };
+    auto values = [&](int c) {
+        return Values{reinterpret_cast<E *>(
+            lds + 2 * kBuffer + (L::kShared ? c & 1 : wave) * L::kValueTile)};
+    };
 
     Stage<E, K, kChunk, kThreads> gk, gq;
-    Stage<E, 16 * NT, kChunk, 64> gv;  // this wave's values
+    Stage<E, L::kValueCols, kChunk, L::kShared ? kThreads : 64> gv;
+    const int vtid = L::kShared ? tid : lane;
     u32x4 gr[L::kRecPer];
     float gs = 0.f, last_next = 0.f;
     auto fetch_rows = [&](int c) {
@@ -256,7 +276,10 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         if constexpr (L::kRecord) {
             const Buffer b(r, c < chunks ? Rec::kBytes : 0);
 #pragma unroll
-            for (int i = 0; i < L::kRecPer; ++i) gr[i] = b.load16((tid + i * kThreads) * 16);
+            for (int i = 0; i < L::kRecPer; ++i) {
+                const int at = (tid + i * kThreads) * 16;
+                gr[i] = b.load16(at < Rec::kP ? at : at + L::kPBytes);
+            }
         } else {
             gs = Buffer(r + Rec::kScalars, c < chunks ? kScalarSpace : 0).load_float(tid * 4);
         }
@@ -268,13 +291,13 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         if constexpr (L::kRecord) {
 #pragma unroll
             for (int i = 0; i < L::kRecPer; ++i)
-                *reinterpret_cast<u32x4 *>(b + 2 * kTile + (tid + i * kThreads) * 16) = gr[i];
+                *reinterpret_cast<u32x4 *>(b + L::kRows + (tid + i * kThreads) * 16) = gr[i];
         } else {
-            reinterpret_cast<float *>(b + 2 * kTile)[tid] = gs;
+            reinterpret_cast<float *>(b + L::kRows)[tid] = gs;
         }
     };
     auto fetch_values = [&](int c) {
-        gv.load(vp + (long long)c * kChunk * p.v_stride, p.v_stride, step ? 0 : live_of(c), lane);
+        gv.load(vp + (long long)c * kChunk * p.v_stride, p.v_stride, step ? 0 : live_of(c), vtid);
         if constexpr (!L::kRecord)
             last_next = Buffer(rec + c * rec_step + Rec::kScalars + kScalarSpace, c < chunks ? 4 : 0)
                             .load_float(0);
@@ -293,89 +316,81 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
     };
     if (chunks > 0) {
         fetch_rows(0);
-        put_rows(0);
-        // in the loop's order, and as many accesses behind the rows' loads, so that the
-        // loop waits for no more than it needs
-        fetch_rows(1);
-        fetch_values(0);
-        if (MODE != kSummary) {
-            const Buffer none(op, 0);
-#pragma unroll
-            for (int i = 0; i < 4 * NT; ++i) none.store4(0, zero(), E());
+        if constexpr (L::kShared) {
+            fetch_values(0);
+            gv.store(values(0), vtid);
         }
+        put_rows(0);
+        fetch_rows(1);
+        fetch_values(L::kShared ? 1 : 0);
+        // as many accesses behind these loads as the loop has, so that it waits for no
+        // more than it needs
+        const Buffer none(op, 0);
+#pragma unroll
+        for (int i = 0; i < kStores; ++i) none.store16(0, u32x4{0u, 0u, 0u, 0u});
     }
+    // o of chunk c from shared memory, by the threads that put values in its place next
+    auto store_o = [&](int c) {
+        gv.store_rows(values(c), op + (long long)c * kChunk * row, row, c < 0 ? 0 : live_of(c), vtid);
+    };
     for (int c = 0; c < chunks; ++c) {
         const int live = live_of(c);
         __syncthreads();  // buffer c is whole, and the other one has been read
+        if constexpr (L::kShared) store_o(c - 1);
         put_rows(c + 1);
+        if constexpr (L::kShared) gv.store(values(c + 1), vtid);
         if constexpr (!L::kRecord) fetch_T(c);
         fetch_rows(c + 2);
+        if constexpr (L::kShared) fetch_values(c + 2);
         const char *buf = buffer(c);
         const Tile<E, K> tk{reinterpret_cast<E *>(const_cast<char *>(buf))},
             tq{reinterpret_cast<E *>(const_cast<char *>(buf) + kTile)};
-        const char *rc = buf + 2 * kTile;
-        const Scalars &sc = *reinterpret_cast<const Scalars *>(L::kRecord ? rc + Rec::kScalars : rc);
-        gv.store(tv, lane);  // read by this wave alone
+        const char *rc = buf + L::kRows;
+        const Scalars &sc = *reinterpret_cast<const Scalars *>(L::kRecord ? rc + L::kScalarsAt : rc);
+        const Values tv = values(c);
+        if constexpr (!L::kShared) gv.store(tv, vtid);  // read by this wave alone
         const float last = L::kRecord ? sc.last : last_next;
         const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)];
-        fetch_values(c + 1);
+        if constexpr (!L::kShared) fetch_values(c + 1);
         if (MODE == kTrain)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                store_rounded<E>(S[n], states + (size_t)c * p.Hv * state_size + 16 * n * K, g, lo);
+            store_rounded<E>(S, states + (size_t)c * p.Hv * state_size, g, lo);
 
         // X = K S0^T [tokens, values]; O^T = S0 Q^T [values, tokens], so that a lane
         // ends up with four neighbouring values of a token
-        f32x4 X[4][NT], O[4][NT], R[4][NT];
+        f32x4 X[4], O[4], R[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) X[i][n] = O[i][n] = zero();
+        for (int i = 0; i < 4; ++i) X[i] = O[i] = zero();
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            Split<E> b[NT];
             Frag<E> fk[4], fq[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 fk[i] = tk.rows(tile_row(i, lo), 32 * ks, g);
                 if (MODE != kSummary) fq[i] = tq.rows(tile_row(i, lo), 32 * ks, g);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(S[n].t[2 * ks], S[n].t[2 * ks + 1]);
+            const Split<E> b = to_split<E>(S.t[2 * ks], S.t[2 * ks + 1]);
 #pragma unroll
             for (int part = 0; part < kPartsMixed<E>; ++part)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        X[i][n] = mma_mixed(part, fk[i], b[n], X[i][n]);
+                for (int i = 0; i < 4; ++i) X[i] = mma_mixed(part, fk[i], b, X[i]);
             if (MODE != kSummary)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) O[i][n] = mma(b[n].hi, fq[i], O[i][n]);
+                for (int i = 0; i < 4; ++i) O[i] = mma(b.hi, fq[i], O[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float qs = sc.qS[tile_row(i, lo)];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                R[i][n] = tv.template column4<4>(tile_row(i, 4 * g), 16 * n, lane) +
-                          row_bcast4(kS, i) * X[i][n];
-                if (MODE != kSummary) O[i][n] *= qs;
-            }
+            R[i] = tv.template column4<4>(tile_row(i, 4 * g), vcol, lane) + row_bcast4(kS, i) * X[i];
+            if (MODE != kSummary) O[i] *= qs;
         }
+        if (MODE != kSummary) __builtin_amdgcn_sched_barrier(0);
         if constexpr (!L::kRecord && MODE != kSummary) fetch_P(c);
-        f32x4 U[4][NT];
+        f32x4 U[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) U[i][n] = zero();
+        for (int i = 0; i < 4; ++i) U[i] = zero();
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            Split<E> b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = to_split<E>(R[2 * st][n], R[2 * st + 1][n]);
+            const Split<E> b = to_split<E>(R[2 * st], R[2 * st + 1]);
             if constexpr (L::kRecord)
 #pragma unroll
                 for (int f = 0; f < 6; ++f)
@@ -385,22 +400,15 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
 #pragma unroll
                 for (int f = 0; f < 6; ++f)
                     if (kLowStep[f] == st)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            U[kLowTile[f]][n] = mma_split(part, T[f], b[n], U[kLowTile[f]][n]);
+                        U[kLowTile[f]] = mma_split(part, T[f], b, U[kLowTile[f]]);
         }
         // the state
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < K / 16; ++m) S[n].t[m] *= last;
+        for (int m = 0; m < K / 16; ++m) S.t[m] *= last;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            Split<E> b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                b[n] = to_split<E>(row_bcast4(kD, 2 * st) * U[2 * st][n],
-                                   row_bcast4(kD, 2 * st + 1) * U[2 * st + 1][n]);
+            const Split<E> b = to_split<E>(row_bcast4(kD, 2 * st) * U[2 * st],
+                                           row_bcast4(kD, 2 * st + 1) * U[2 * st + 1]);
 #pragma unroll
             for (int half = 0; half < K / 64; ++half) {  // four tiles of keys at a time
                 Frag<E> a[4];
@@ -411,47 +419,43 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
                 for (int part = 0; part < kPartsMixed<E>; ++part)
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            S[n].t[4 * half + m] = mma_mixed(part, a[m], b[n], S[n].t[4 * half + m]);
+                        S.t[4 * half + m] = mma_mixed(part, a[m], b, S.t[4 * half + m]);
             }
+        }
+        if (MODE == kTrain) {
+            const Buffer bu(up + (long long)c * kChunk * row, row_bytes<E>(live, row));
+            store_values(U, tv, vcol, bu, row, lane);
         }
         if (MODE != kSummary) {
             // the readout: O^T += U^T P^T
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                Frag<E> b[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) b[n] = to_frag<E>(U[2 * st][n], U[2 * st + 1][n]);
+                const Frag<E> b = to_frag<E>(U[2 * st], U[2 * st + 1]);
 #pragma unroll
                 for (int f = 0; f < 6; ++f)
                     if (kLowStep[f] == st) {
                         if constexpr (L::kRecord)
                             P[f] = get_frag<E>(rc + Rec::kP + f * Rec::kFragBytes, lane);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            O[kLowTile[f]][n] = mma(b[n], P[f], O[kLowTile[f]][n]);
+                        O[kLowTile[f]] = mma(b, P[f], O[kLowTile[f]]);
                     }
             }
-            const Buffer bo(op + (long long)c * kChunk * row, row_bytes<E>(live, row));
+            if constexpr (L::kShared) {  // in the place of the values
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<u32x2 *>(tv.p + tv.offset(tile_row(i, lo), vcol + 4 * g)) =
+                        u32x2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
+            } else {
+                const Buffer bo(op + (long long)c * kChunk * row, row_bytes<E>(live, row));
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    bo.store4((unsigned)(tile_row(i, lo) * row + 16 * n + 4 * g) *
-                                  (unsigned)sizeof(E), O[i][n], E());
+                for (int i = 0; i < 4; ++i)
+                    bo.store4((unsigned)(tile_row(i, lo) * row + 4 * g) * (unsigned)sizeof(E), O[i],
+                              E());
+            }
         }
-        if (MODE == kTrain) {
-            const Buffer bu(up + (long long)c * kChunk * row, row_bytes<E>(live, row));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        bu.store1((unsigned)(tile_row(i, 4 * g + e) * row + 16 * n + lo) *
-                                      (unsigned)sizeof(E), U[i][n][e], E());
-        }
+    }
+    if (L::kShared && chunks > 0) {
+        __syncthreads();
+        store_o(chunks - 1);
     }
     float *to = nullptr;
     if (MODE == kSummary) {
@@ -459,24 +463,22 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
             constexpr int kPlanes = sizeof(E) == 2 ? 2 : 1;
             E *plane = static_cast<E *>(p.seg_step) +
                        ((size_t)seg_slot * p.Hv + hv) * (kPlanes * K * K) + (size_t)value0 * K;
-            if (value0 < K)
+            if (value0 < K) {
+                store_rounded<E>(S, plane, g, lo);
+                if constexpr (kPlanes == 2) {
+                    State<K> low;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    store_rounded<E>(S[n], plane + 16 * n * K, g, lo);
-                    if constexpr (kPlanes == 2) {
-                        State<K> low;
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const Frag<E> hi = to_frag<E>(S.t[2 * ks], S.t[2 * ks + 1]);
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const Frag<E> hi = to_frag<E>(S[n].t[2 * ks], S[n].t[2 * ks + 1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                low.t[2 * ks][e] = S[n].t[2 * ks][e] - hi.at(e);
-                                low.t[2 * ks + 1][e] = S[n].t[2 * ks + 1][e] - hi.at(4 + e);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            low.t[2 * ks][e] = S.t[2 * ks][e] - hi.at(e);
+                            low.t[2 * ks + 1][e] = S.t[2 * ks + 1][e] - hi.at(4 + e);
                         }
-                        store_rounded<E>(low, plane + K * K + 16 * n * K, g, lo);
                     }
+                    store_rounded<E>(low, plane + K * K, g, lo);
                 }
+            }
             return;
         }
         to = p.seg_state + ((size_t)seg_slot * p.Hv + hv) * state_size;
@@ -484,9 +486,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         const int out = slot_of(p.slots_out, seq, p.pool);
         if (out >= 0) to = p.s_out + ((size_t)out * p.Hv + hv) * state_size;
     }
-    if (to)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) store_state(S[n], to + (size_t)(value0 + 16 * n) * K, g, lo);
+    if (to) store_state(S, to + (size_t)value0 * K, g, lo);
 }
 
 // From the segments' summaries to the states at their ends, in place: the state
@@ -682,18 +682,13 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
         {
             const Buffer bv(dvp + (long long)c * kChunk * row, row_bytes<E>(live, row)),
                 br(drp + (long long)c * kChunk * row, row_bytes<E>(live, row));
+            store_values(R, to, 0, br, row, lane);
+            f32x4 dv[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t0 = tile_row(i, 4 * g);
-                const f32x4 be = row_bcast4(beta, i);
+            for (int i = 0; i < 4; ++i) dv[i] = row_bcast4(beta, i) * R[i];
+            store_values(dv, to, 0, bv, row, lane);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const unsigned off = (unsigned)((t0 + e) * row + lo) * (unsigned)sizeof(E);
-                    br.store1(off, R[i][e], E());
-                    bv.store1(off, be[e] * R[i][e], E());
-                }
-                R[i] *= row_bcast4(kS, i);
-            }
+            for (int i = 0; i < 4; ++i) R[i] *= row_bcast4(kS, i);
         }
         // dS0 = c_C D + dO^T diag(scale c / |q|) Q - dR^T diag(beta c / |k|) K
 #pragma unroll
@@ -729,8 +724,7 @@ constexpr int chain_lds() {
 template <class F>
 hipError_t launch(F fn, size_t blocks, int threads, int lds, const ChainArgs &a,
                   hipStream_t stream) {
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(fn), lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), lds, stream, a);
     return hipGetLastError();
@@ -739,11 +733,11 @@ hipError_t launch(F fn, size_t blocks, int threads, int lds, const ChainArgs &a,
 template <class E, int K, int W>
 hipError_t launch_forward_t(const ChainArgs &a, bool train, int units, int n_seq,
                             hipStream_t stream) {
-    constexpr int kLds = ForwardLds<E, K, W>::kBytes;
     const int parts = a.V / (16 * W), step_parts = (K + 16 * W - 1) / (16 * W);
     if (a.seg) {
         hipError_t e = launch(forward_chain_kernel<E, K, W, kSummary>,
-                              (size_t)units * a.Hv * (parts + step_parts), 64 * W, kLds, a, stream);
+                              (size_t)units * a.Hv * (parts + step_parts), 64 * W,
+                      ForwardLds<E, K, W, kSummary>::kBytes, a, stream);
         if (e != hipSuccess) return e;
         e = launch(combine_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / 64), kThreads,
                    (sizeof(E) == 2 ? 2 : 1) * tile_bytes<E, K>(K), a, stream);
@@ -751,7 +745,8 @@ hipError_t launch_forward_t(const ChainArgs &a, bool train, int units, int n_seq
     }
     return launch(train ? forward_chain_kernel<E, K, W, kTrain>
                         : forward_chain_kernel<E, K, W, kInfer>,
-                  (size_t)units * a.Hv * parts, 64 * W, kLds, a, stream);
+                  (size_t)units * a.Hv * parts, 64 * W, ForwardLds<E, K, W, kInfer>::kBytes, a,
+                  stream);
 }
 
 template <class E, int K>
@@ -771,19 +766,28 @@ ChainArgs chain_args(const Problem &p) {
 
 }  // namespace
 
-// Waves of a forward workgroup: eight where whole workgroups of 128 values come out
-// (two waves per SIMD share one copy of the chunk); float tiles leave room for four.
-bool wide(const Problem &p) { return p.bf16 && p.V % 128 == 0; }
-
+// How the forward pass is split.  A workgroup has eight waves where whole ones of 128
+// values come out (two waves per SIMD share one copy of the chunk; float tiles
+// leave room for four), unless those would be fewer than the CUs: four sequences of 32
+// heads and 2048 tokens (training) took 194 us with 128 workgroups of eight, 139 us with
+// 256 of four.  Few long sequences are done in segments: an extra pass for the
+// segments' summaries costs about what the pass over them does, so there have to be
+// four segments a sequence, long enough for the launches: 8 heads of 128 values,
+// two sequences of up to 1001 tokens took 102 us whole and 54 us in segments (float), 34 us
+// either way with 128 tokens a segment in bf16, which has shorter chunks.
 Segments plan_segments(const Problem &p) {
     Segments s{};
     s.units = p.n_seq;
-    const long long chains = (long long)p.n_seq * p.Hv * (p.V / (wide(p) ? 128 : 64));
+    s.waves = p.bf16 && p.V % 128 == 0 ? 8 : 4;
+    const long long chains = (long long)p.n_seq * p.Hv * (p.V / (16 * s.waves));
     const long long average = p.total / p.n_seq;
-    if (chains > 64 || average < kMinSegment * 2) return s;
-    long long n = 256 / chains;                     // segments of an average sequence
-    if (n > average / kMinSegment) n = average / kMinSegment;
-    if (n < 2) return s;
+    const int shortest = p.bf16 ? 256 : 64;  // tokens of a segment
+    long long n = kCus / chains;             // segments of an average sequence
+    if (n > average / shortest) n = average / shortest;
+    if (n < 4) {
+        if (chains < kCus) s.waves = 4;
+        return s;
+    }
     const long long len = (average + n - 1) / n;
     s.seg = (int)((len + kChunk - 1) / kChunk * kChunk);
     s.units = p.cu ? p.total / s.seg + p.n_seq : p.n_seq * ((p.T + s.seg - 1) / s.seg);
@@ -811,7 +815,7 @@ hipError_t launch_forward(const ForwardArgs &f, hipStream_t stream) {
     if (!p.bf16)
         return p.K == 64 ? launch_forward_t<float, 64, 4>(a, train, u, n, stream)
                          : launch_forward_t<float, 128, 4>(a, train, u, n, stream);
-    if (wide(p))
+    if (s.waves == 8)
         return p.K == 64 ? launch_forward_t<bf16_t, 64, 8>(a, train, u, n, stream)
                          : launch_forward_t<bf16_t, 128, 8>(a, train, u, n, stream);
     return p.K == 64 ? launch_forward_t<bf16_t, 64, 4>(a, train, u, n, stream)

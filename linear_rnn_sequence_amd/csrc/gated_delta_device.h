@@ -192,9 +192,18 @@ __device__ __forceinline__ Split<float> to_split<float>(f32x4 a, f32x4 b) {
 // ---------------------------------------------------------------------------
 struct Buffer {
     __amdgpu_buffer_rsrc_t r;
+    // base and bytes are the same for all lanes, which the compiler does not always
+    // see (it would then loop over the lanes at every access)
     __device__ __forceinline__ Buffer(const void *base, unsigned bytes)
-        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
+        : r(__builtin_amdgcn_make_buffer_rsrc(uniform(base), (short)0,
+                                              __builtin_amdgcn_readfirstlane((int)bytes),
                                               0x00020000)) {}
+    static __device__ __forceinline__ void *uniform(const void *p) {
+        const unsigned long long u = reinterpret_cast<unsigned long long>(p);
+        const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)u),
+                       hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32));
+        return reinterpret_cast<void *>((unsigned long long)hi << 32 | lo);
+    }
     __device__ __forceinline__ u32x4 load16(unsigned off) const {
         return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
     }
@@ -209,12 +218,8 @@ struct Buffer {
     __device__ __forceinline__ void store4(unsigned off, f32x4 x, float) const {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, (int)off, 0, 0);
     }
-    // one element
-    __device__ __forceinline__ void store1(unsigned off, float x, bf16_t) const {
-        __builtin_amdgcn_raw_buffer_store_b16((short)cvt_pk(x, x), r, (int)off, 0, 0);
-    }
-    __device__ __forceinline__ void store1(unsigned off, float x, float) const {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, (int)off, 0, 0);
+    __device__ __forceinline__ void store16(unsigned off, u32x4 x) const {
+        __builtin_amdgcn_raw_buffer_store_b128(x, r, (int)off, 0, 0);
     }
 };
 
@@ -335,7 +340,49 @@ struct Stage {
                 t.p + t.offset(piece / kRowPieces, piece % kRowPieces * kPiece)) = x[i];
         }
     }
+    // the way back: `live` rows of the tile to rows `stride` elements apart
+    static __device__ __forceinline__ void store_rows(Tile<E, C> t, E *dst, int stride, int live,
+                                                      int tid) {
+        const Buffer b(dst, row_bytes<E>(live, stride));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int piece = tid + i * THREADS;
+            const int row = piece / kRowPieces, col = piece % kRowPieces * kPiece;
+            b.store16((unsigned)(row * stride + col) * (unsigned)sizeof(E),
+                      *reinterpret_cast<const u32x4 *>(t.p + t.offset(row, col)));
+        }
+    }
 };
+
+// Stores a wave's 16 values of 64 tokens, which lie in result tiles [tokens, values],
+// by way of 16 columns of shared memory that are its own: pieces of 16 bytes, where
+// the lanes' single elements would be four rows of 32 bytes an instruction.
+template <class E, int C>
+__device__ __forceinline__ void store_values(const f32x4 (&x)[4], Tile<E, C> t, int col0,
+                                             const Buffer &b, int stride, int lane) {
+    constexpr int kPiece = Tile<E, C>::kPiece, kRowPieces = 16 / kPiece;
+    const int g = lane >> 4, lo = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const int row = tile_row(i, 4 * g + e);
+            if constexpr (sizeof(E) == 2) {
+                const unsigned u = cvt_pk(x[i][e], x[i][e + 1]);
+                t.p[t.offset(row, col0 + lo)] = (bf16_t)u;
+                t.p[t.offset(row + 1, col0 + lo)] = (bf16_t)(u >> 16);
+            } else {
+                t.p[t.offset(row, col0 + lo)] = x[i][e];
+                t.p[t.offset(row + 1, col0 + lo)] = x[i][e + 1];
+            }
+        }
+#pragma unroll
+    for (int j = 0; j < kRowPieces; ++j) {
+        const int piece = lane + 64 * j, row = piece / kRowPieces, col = piece % kRowPieces * kPiece;
+        b.store16((unsigned)(row * stride + col) * (unsigned)sizeof(E),
+                  *reinterpret_cast<const u32x4 *>(t.p + t.offset(row, col0 + col)));
+    }
+}
 
 // Reciprocal norms of 64 rows, four lanes of 256 threads per row (1 without
 // normalisation; 0 for the rows behind the sequence's end).
@@ -411,10 +458,10 @@ struct Layout {
     }
 };
 
-// Inclusive sums of the chunk's log decays, lane = token, in float64 and kept as two
-// floats: the decay between two tokens is the exponential of a difference of these
-// sums, which in one float would lose what a strong decay before both of them
-// took.  exp(-200) is zero in float32, so a log decay below that (-infinity, the
+// Inclusive sums of the chunk's log decays (to the base 2), lane = token, in float64
+// and kept as two floats: the decay between two tokens is the power of two of a
+// difference of these sums, which in one float would lose what a strong decay
+// before both of them took.  exp(-200) is zero in float32, so a log decay below that (-infinity, the
 // type's lowest value) is raised to it; a NaN stays one.
 constexpr float kLowestLogDecay = -200.f;
 template <int CTRL, int ROWS>
@@ -436,6 +483,7 @@ __device__ __forceinline__ Sum2 scan_decay(float g) {
     x += dpp_from<0x118, 0xF>(x);
     x += dpp_from<0x142, 0xA>(x);  // lane 15 of rows 0 and 2 to rows 1 and 3
     x += dpp_from<0x143, 0xC>(x);  // lane 31 to rows 2 and 3
+    x *= 1.4426950408889634;
     const float hi = (float)x;
     return Sum2{hi, (float)(x - hi)};
 }
@@ -444,6 +492,10 @@ __device__ __forceinline__ float last_lane(float x) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 __device__ __forceinline__ Sum2 last_lane(Sum2 x) { return Sum2{last_lane(x.hi), last_lane(x.lo)}; }
+__device__ __forceinline__ Sum2 lane_of(Sum2 x, int lane) {  // a lane's number for all
+    return Sum2{__int_as_float(__builtin_amdgcn_readlane(__float_as_int(x.hi), lane)),
+                __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x.lo), lane))};
+}
 // inclusive sums over the lanes
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_from(float x) {
@@ -460,9 +512,9 @@ __device__ __forceinline__ float scan_lanes(float x) {
     return x;
 }
 __device__ __forceinline__ float decay(Sum2 to, Sum2 from) {
-    return __expf((to.hi - from.hi) + (to.lo - from.lo));
+    return __builtin_amdgcn_exp2f((to.hi - from.hi) + (to.lo - from.lo));
 }
-__device__ __forceinline__ float decay(Sum2 to) { return __expf(to.hi + to.lo); }
+__device__ __forceinline__ float decay(Sum2 to) { return __builtin_amdgcn_exp2f(to.hi + to.lo); }
 
 // Value of lane N of each row of 16 lanes, for a product's operand (DPP row_newbcast).
 // A wave that keeps a number per token in the lane own_token(lane) has those of the

@@ -463,8 +463,7 @@ template <class E, int K>
 hipError_t launch_gradients_t(const GradArgs &a, int slots, hipStream_t stream) {
     constexpr int kLds = GradLds<E, K>::kBytes;
     const auto fn = gradient_kernel<E, K>;
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(fn), kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(fn, dim3((unsigned)((size_t)slots * a.Hk)), dim3(kThreads), kLds, stream, a);
     return hipGetLastError();

@@ -51,14 +51,22 @@ struct DecodeArgs {
     void *o;
 };
 
-// How the forward splits the sequences: segments of `seg` tokens (0: none), `units`
+// How the forward splits its work: waves of a workgroup, segments of `seg` tokens (0: none), `units`
 // of them at most, and the bytes of their states and transitions.
 struct Segments {
-    int seg, units;
+    int waves, seg, units;
     size_t state_bytes, step_bytes;
 };
-constexpr int kMinSegment = 512;  // tokens
+constexpr int kCus = 256;
 Segments plan_segments(const Problem &p);
+
+// lets a kernel have `bytes` of shared memory (it may have 64 KiB with its static arrays,
+// none of which come to 16 KiB, anyway)
+inline hipError_t allow_lds(const void *kernel, int bytes) {
+    return bytes <= 48 * 1024 ? hipSuccess
+                              : hipFuncSetAttribute(
+                                    kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 size_t forward_record_bytes(bool bf16);
 size_t backward_record_bytes(bool bf16);

@@ -9,13 +9,21 @@
 // chain kernels need T and P (forward) or T^T and P^T (backward) as matrix-core
 // operands, so they are written in that order, with the chunk's scalars.
 //
-// One workgroup of four waves per chunk and key head; it forms the products
-// k.k and q.k once and then goes through the value heads that share the key
-// head.  T by blocks of 16: wave w inverts the diagonal block w (tri_inverse),
-// then owns the blocks below it in its block column,
+// One workgroup of four waves per chunk and key head; it forms the products k.k and
+// q.k once and then goes through the value heads that share the key head.  Wave w
+// has the rows 16w .. of A and the tokens 16 (3 - w) .. of P, so that each has
+// five of the lower triangle's tiles.
+//
+// T by blocks of 16: wave w inverts the diagonal block w (tri_inverse), then owns
+// the blocks below it in its block column,
 //   T_ij = -T_ii sum_{j <= k < i} A_ik T_kj,
 // whose products take T_kj from registers (float32 matrix cores, so T keeps
 // float32 accuracy also where keys are alike and A is not small).
+//
+// What bounds the kernel is the number of vector instructions, most of them for the
+// decays.  So outside the diagonal blocks E_ts is a product of two numbers, from s
+// to the end of its block of 16 and from there to t (both at most 1), of which
+// there are few: a table per value head, with the other factors of t and of s in it.
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
@@ -44,28 +52,55 @@ __device__ __forceinline__ f32x4 mul_block(const float *m, int row0, int col0, f
     return c;
 }
 
+// Four neighbouring elements of an operand lane (the lower or upper half of its
+// eight), rounded to E or split.
+template <class E, bool SPLIT>
+__device__ __forceinline__ void put_quad(char *frag, int at_lane, int upper, f32x4 v) {
+    if constexpr (sizeof(E) == 4) {
+        *reinterpret_cast<f32x4 *>(frag + upper * 1024 + at_lane * 16) = v;
+    } else {
+        char *at = frag + at_lane * 16 + upper * 8;
+        const u32x2 hi{cvt_pk(v[0], v[1]), cvt_pk(v[2], v[3])};
+        *reinterpret_cast<u32x2 *>(at) = hi;
+        if constexpr (SPLIT)
+            *reinterpret_cast<u32x2 *>(at + 1024) =
+                u32x2{cvt_pk(v[0] - wkv7::bf16_lo(hi[0]), v[1] - wkv7::bf16_hi(hi[0])),
+                      cvt_pk(v[2] - wkv7::bf16_lo(hi[1]), v[3] - wkv7::bf16_hi(hi[1]))};
+    }
+}
+
+// T and A share one array: A's blocks (i, j), i > j, lie in their place, T's diagonal
+// blocks on the diagonal, and T_ij, i > j, as it is in the place (j, i).
 template <class E, int K>
 constexpr int prep_lds() {
-    // A and T take the place of the k and q rows once their products are formed
-    constexpr int rows = 2 * tile_bytes<E, K>(kChunk), mats = 2 * kChunk * kPitchA * 4;
+    // they take the place of the k and q rows once those products are formed
+    constexpr int rows = 2 * tile_bytes<E, K>(kChunk), mats = kChunk * kPitchA * 4;
     return rows > mats ? rows : mats;
 }
+
+// of one value head; block x ends at token 16x + 15
+struct Decays {
+    Sum2 G[kChunk];
+    float beta[kChunk];
+    float toA[3][kChunk];   // beta_t / |k_t| times the decay from block x's end to t
+    float toP[3][kChunk];   // scale / |q_t| times that
+    float from[kChunk];     // 1 / |k_s| times the decay from s to its block's end
+};
 
 template <class E, int K, bool BWD>
 __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
     using Rec = typename std::conditional<BWD, BwdRecord<E>, FwdRecord<E>>::type;
     extern __shared__ __align__(16) char lds[];
-    Tile<E, K> tk{reinterpret_cast<E *>(lds)};
-    Tile<E, K> tq{reinterpret_cast<E *>(lds + tile_bytes<E, K>(kChunk))};
+    const Tile<E, K> tk{reinterpret_cast<E *>(lds)};
+    const Tile<E, K> tq{reinterpret_cast<E *>(lds + tile_bytes<E, K>(kChunk))};
     float *sA = reinterpret_cast<float *>(lds);
-    float *sT = sA + kChunk * kPitchA;
-    constexpr int kHeads = 4;  // value heads whose decays are summed at a time
-    __shared__ Sum2 sG4[kHeads][kChunk];
-    __shared__ __align__(16) float sBeta4[kHeads][kChunk];
-    __shared__ float sRk[kChunk], sRq[kChunk];
+    constexpr int kHeads = 2;  // value heads whose tables are made at a time
+    __shared__ __align__(16) Decays sD[kHeads];
+    __shared__ __align__(16) float sRk[kChunk];
+    __shared__ __align__(16) float sRq[kChunk];
 
-    const int tid = threadIdx.x, lane = tid & 63,
-              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, lo = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), pt = 3 - wave;
     const int slot = (int)(blockIdx.x / p.Hk), hk = (int)(blockIdx.x % p.Hk);
     Seq sq;
     p.lay.find(slot, kChunk, sq);
@@ -74,7 +109,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
     const int live = sq.end - first < kChunk ? sq.end - first : kChunk;
     const int rep = p.Hv / p.Hk;
 
-    // the first four value heads' gates, wave by wave
+    // two value heads' gates, one for each of the last two waves
     float gate = 0.f, strength = 0.f;
     auto load_gates = [&](int r) {
         const size_t at = ((size_t)first + lane) * p.Hv + hk * rep + r;
@@ -82,7 +117,36 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
         gate = in ? to_float(static_cast<const E *>(p.g)[at]) : 0.f;
         strength = in ? to_float(static_cast<const E *>(p.beta)[at]) : 0.f;
     };
-    load_gates(wave);
+    // a head's table, and the scalars of its record
+    auto make_table = [&](int r) {
+        Decays &d = sD[r % kHeads];
+        const Sum2 G = scan_decay(gate);
+        const float rk = sRk[lane], rq = p.scale * sRq[lane], from0 = decay(G);
+        d.G[lane] = G;
+        d.beta[lane] = strength;
+        const Sum2 end[4] = {lane_of(G, 15), lane_of(G, 31), lane_of(G, 47), lane_of(G, 63)};
+        float c = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float down = decay(end[x], G), on = decay(G, end[x]);
+            c = lane / 16 == x ? down : c;
+            if (x < 3) {
+                d.toA[x][lane] = lane / 16 > x ? strength * rk * on : 0.f;
+                d.toP[x][lane] = lane / 16 > x ? rq * on : 0.f;
+            }
+        }
+        d.from[lane] = c * rk;
+        if (r < rep) {
+            Scalars *sc = reinterpret_cast<Scalars *>(
+                p.records + ((size_t)slot * p.Hv + hk * rep + r) * Rec::kBytes + Rec::kScalars);
+            sc->beta[lane] = strength;
+            sc->kS[lane] = -(BWD ? strength : 1.f) * from0 * rk;
+            sc->kD[lane] = decay(end[3], G) * rk;
+            sc->qS[lane] = from0 * rq;
+            if (lane == 63) sc->last = from0;
+        }
+    };
+    if (wave >= 2) load_gates(wave - 2);
     {
         Stage<E, K, kChunk, 256> sk, sqv;
         sk.load(static_cast<const E *>(p.k) + (long long)first * p.k_stride + hk * K, p.k_stride,
@@ -101,150 +165,138 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
             sRq[tid >> 2] = b;
         }
     }
-    // k.k: rows 16 wave + 4g + e, columns 16 j + lo, j <= wave (natural order)
-    f32x4 kk[4];
+    // kk: k.k, rows 16 wave + 4g + e, columns 16 j + lo, j <= wave.  qk: q.k with the
+    // tokens 16 pt + lo as columns and s = 16 j + 4g + e as rows, j <= pt, or (backward)
+    // with s = 16 pt + lo as columns and t = 16 j + 4g + e as rows, j >= pt.
+    f32x4 kk[4], qk[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // P: this wave forms the fragments f = wave, wave + 4 of the six.  The fragment's
-    // two result tiles are those of P^T (forward: rows s, columns t) or P
-    // (backward: rows t, columns s), rows in tile_row order.
-    f32x4 qk[2][2];
+    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int pc = BWD ? wave : pt;  // the block of those columns: five tiles with kk's again
+    {
+        const Tile<E, K> ta = BWD ? tq : tk, tb = BWD ? tk : tq;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+        for (int ks = 0; ks < K / 32; ++ks) {
+            const Frag<E> a = tk.rows(16 * wave + lo, 32 * ks, g),
+                          b = tb.rows(16 * pc + lo, 32 * ks, g);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) qk[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < K / 32; ++ks) {
-        const Frag<E> a = tk.rows(16 * wave + lo, 32 * ks, g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= wave) kk[j] = mma(a, tk.rows(16 * j + lo, 32 * ks, g), kk[j]);
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int f = wave + 4 * n;
-            if (f >= 6) break;
-            const int tile = BWD ? kUpTile[f] : kLowTile[f], step = BWD ? kUpStep[f] : kLowStep[f];
-            const Tile<E, K> ta = BWD ? tq : tk, tb = BWD ? tk : tq;
-            const Frag<E> b = tb.rows(tile_row(tile, lo), 32 * ks, g);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                qk[n][h] = mma(ta.rows(tile_row(2 * step + h, lo), 32 * ks, g), b, qk[n][h]);
+            for (int j = 0; j < 4; ++j) {
+                if (j <= wave) kk[j] = mma(a, tk.rows(16 * j + lo, 32 * ks, g), kk[j]);
+                if (BWD ? j >= pc : j <= pc)
+                    qk[j] = mma(ta.rows(16 * j + lo, 32 * ks, g), b, qk[j]);
+            }
         }
     }
-    __syncthreads();
-    // blocks (0, 1) and (2, 3) of T: read as zeros, never written
-    if (tid < 128) {
-        const int row = 32 * (tid >> 6) + (tid & 15), col = row / 32 * 32 + 16 + 4 * (tid >> 4 & 3);
-        *reinterpret_cast<f32x4 *>(sT + row * kPitchA + col) = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    __syncthreads();  // the norms; the rows have been read
 
     for (int r = 0; r < rep; ++r) {
         const int hv = hk * rep + r;
         char *rec = p.records + ((size_t)slot * p.Hv + hv) * Rec::kBytes;
+        if (r) __syncthreads();  // the last head's reads of sA and of its table
         if (r % kHeads == 0) {
-            if (r) __syncthreads();  // the last heads' reads of sG4, sBeta4
-            if (r) load_gates(r + wave);
-            if (r + wave < rep) {
-                const Sum2 G = scan_decay(gate);
-                sG4[wave][lane] = G;
-                sBeta4[wave][lane] = strength;
-                Scalars *sc = reinterpret_cast<Scalars *>(rec + wave * Rec::kBytes + Rec::kScalars);
-                const float from0 = decay(G);
-                sc->beta[lane] = strength;
-                sc->kS[lane] = -(BWD ? strength : 1.f) * from0 * sRk[lane];
-                sc->kD[lane] = decay(last_lane(G), G) * sRk[lane];
-                sc->qS[lane] = p.scale * from0 * sRq[lane];
-                if (lane == 63) sc->last = from0;
+            if (wave >= 2) {
+                if (r) load_gates(r + wave - 2);
+                make_table(r + wave - 2);
             }
+            __syncthreads();
         }
-        __syncthreads();  // the above; the last head's reads of sA, sT
-        const Sum2 *sG = sG4[r % kHeads];
-        const float *sBeta = sBeta4[r % kHeads];
-        f32x4 nd{0.f, 0.f, 0.f, 0.f}, ndt{0.f, 0.f, 0.f, 0.f};
+        const Decays &d = sD[r % kHeads];
+        f32x4 x, xt;
         {
-            Sum2 Gr[4];
-            float rr[4], br[4];
+            const int row0 = 16 * wave + 4 * g;
+            f32x4 nd, ndt;
+            const Sum2 Gc = d.G[16 * wave + lo];
+            const float rc = sRk[16 * wave + lo], bc = d.beta[16 * wave + lo];
+            const f32x4 rr = *reinterpret_cast<const f32x4 *>(sRk + row0),
+                        br = *reinterpret_cast<const f32x4 *>(d.beta + row0);
+            f32x4 diag = kk[0];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 16 * wave + 4 * g + e;
-                Gr[e] = sG[row];
-                rr[e] = sRk[row];
-                br[e] = sBeta[row];
+            for (int j = 1; j < 4; ++j) diag = j == wave ? kk[j] : diag;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // the diagonal block, and its transpose
+                const Sum2 Gr = d.G[row0 + e];
+                const int row = 4 * g + e;
+                const float y =
+                    diag[e] * rr[e] * rc * (row > lo ? decay(Gr, Gc) : decay(Gc, Gr));
+                nd[e] = row > lo ? br[e] * y : 0.f;
+                ndt[e] = row < lo ? bc * y : 0.f;
             }
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                if (j >= wave) break;
+                const f32x4 to = *reinterpret_cast<const f32x4 *>(d.toA[j] + row0);
+                const float from = d.from[16 * j + lo];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sA[(row0 + e) * kPitchA + 16 * j + lo] = kk[j][e] * from * to[e];
+            }
+            wkv7::tri_inverse(nd, ndt, lane, x, xt);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sA[(row0 + e) * kPitchA + 16 * wave + lo] = x[e];
+        }
+        {  // P: a lane's column, its four neighbouring rows of each tile
+            const int col = 16 * pc + lo;
+            const Sum2 Gc = d.G[col];
+            const float factor = BWD ? sRk[col] : p.scale * sRq[col];
+            const float from_col = d.from[col];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (j > wave) break;
-                const int col = 16 * j + lo;
-                const Sum2 Gc = sG[col];
-                const float rc = sRk[col], bc = sBeta[col];
+                // (a block behind the diagonal that shares a fragment with one before it is
+                // written as zeros)
+                if (BWD ? j < (pc & ~1) : j > (pc | 1)) continue;
+                const int row0 = 16 * j + 4 * g;
+                f32x4 v{0.f, 0.f, 0.f, 0.f};
+                if (j == pc) {
+                    const f32x4 rr = *reinterpret_cast<const f32x4 *>((BWD ? sRq : sRk) + row0) *
+                                     (BWD ? p.scale : 1.f) * factor;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 16 * wave + 4 * g + e;
-                    const float x = kk[j][e] * rr[e] * rc;
-                    if (j < wave) {
-                        sA[row * kPitchA + col] = br[e] * decay(Gr[e], Gc) * x;
-                    } else {  // the diagonal block and its transpose stay in registers
-                        const float d = row > col ? decay(Gr[e], Gc) : decay(Gc, Gr[e]);
-                        nd[e] = row > col ? br[e] * d * x : 0.f;
-                        ndt[e] = row < col ? bc * d * x : 0.f;
+                    for (int e = 0; e < 4; ++e) {
+                        const Sum2 Gr = d.G[row0 + e];
+                        const bool in = BWD ? lo <= 4 * g + e : 4 * g + e <= lo;  // s <= t
+                        const float f = rr[e] * (BWD ? decay(Gr, Gc) : decay(Gc, Gr));
+                        v[e] = in ? f * qk[j][e] : 0.f;
+                    }
+                } else if (BWD ? j > pc : j < pc) {
+                    if constexpr (BWD) {  // from column s to rows t
+                        const float *to = d.toP[0] + pc * kChunk;
+                        v = qk[j] * (from_col * *reinterpret_cast<const f32x4 *>(to + row0));
+                    } else {
+                        v = qk[j] * (d.toP[j][col] *
+                                     *reinterpret_cast<const f32x4 *>(d.from + row0));
                     }
                 }
+                // in operand order: fragment (tile of the columns, 32 rows), lane of the
+                // column and of eight rows
+                const int c32 = col & 31;
+                const int tile = 2 * (col >> 5) + (c32 >> 2 & 1), step = row0 >> 5;
+                const int f = BWD ? (tile < 2 ? 2 * tile + step : tile + 2)
+                                  : (tile < 2 ? tile : 2 * tile - 2 + step);
+                const int at_lane = 16 * (row0 >> 3 & 3) + 4 * (c32 >> 3) + (c32 & 3);
+                put_quad<E, BWD>(rec + Rec::kP + f * (BWD ? Rec::kSplitBytes : FwdRecord<E>::kFragBytes),
+                                 at_lane, g & 1, v);
             }
         }
-        f32x4 x, xt;
-        wkv7::tri_inverse(nd, ndt, lane, x, xt);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sT[(16 * wave + 4 * g + e) * kPitchA + 16 * wave + lo] = x[e];
         __syncthreads();
         {  // block column `wave` of T below the diagonal
             f32x4 col[4];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) col[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i) col[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             col[0] = x;
 #pragma unroll
-            for (int d = 1; d < 4; ++d) {
-                const int i = wave + d;
+            for (int n = 1; n < 4; ++n) {
+                const int i = wave + n;
                 if (i >= 4) break;
                 f32x4 acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < d; ++k)
+                for (int k = 0; k < n; ++k)
                     acc = mul_block(sA, 16 * i, 16 * (wave + k), col[k], acc, g, lo);
                 f32x4 t{0.f, 0.f, 0.f, 0.f};
-                t = mul_block(sT, 16 * i, 16 * i, acc, t, g, lo);
+                t = mul_block(sA, 16 * i, 16 * i, acc, t, g, lo);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    col[d][e] = -t[e];
-                    sT[(16 * i + 4 * g + e) * kPitchA + 16 * wave + lo] = -t[e];
+                    col[n][e] = -t[e];
+                    sA[(16 * wave + 4 * g + e) * kPitchA + 16 * i + lo] = -t[e];
                 }
             }
-        }
-        // P needs nothing of T: formed while other waves finish their columns.  The
-        // waves with the fewest blocks above take two fragments each.
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int f = wave + 4 * n;
-            if (f >= 6) break;
-            const int tile = BWD ? kUpTile[f] : kLowTile[f], step = BWD ? kUpStep[f] : kLowStep[f];
-            const int col = tile_row(tile, lo);
-            const Sum2 Gc = sG[col];
-            const float rc = p.scale * (BWD ? sRk[col] : sRq[col]);
-            f32x4 v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = tile_row(2 * step + h, 4 * g + e);
-                    const bool in = BWD ? col <= row : row <= col;  // s <= t
-                    const Sum2 Gr = sG[row];
-                    const float w = rc * (BWD ? sRq[row] : sRk[row]) *
-                                    (BWD ? decay(Gr, Gc) : decay(Gc, Gr));
-                    v[h][e] = in ? w * qk[n][h][e] : 0.f;
-                }
-            if constexpr (BWD)
-                put_split<E>(rec + Rec::kP + f * Rec::kSplitBytes, to_split<E>(v[0], v[1]), lane);
-            else
-                put_frag<E>(rec + Rec::kP + f * FwdRecord<E>::kFragBytes, to_frag<E>(v[0], v[1]),
-                            lane);
         }
         __syncthreads();
 #pragma unroll
@@ -254,15 +306,18 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
             f32x4 v[2];
             if constexpr (BWD) {  // T^T: row s, columns t
                 const int s = tile_row(kUpTile[f], lo), t0 = 32 * kUpStep[f] + 8 * g;
+                const float *src = sA + (s & ~15) * kPitchA + (t0 & ~15) + (s & 15);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = sT[(t0 + j) * kPitchA + s];
+                for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = src[((t0 & 15) + j) * kPitchA];
+                if (t0 / 16 < s / 16) v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f};
             } else {
-                const int s0 = 32 * kLowStep[f] + 8 * g;
-                const float *src = sT + tile_row(kLowTile[f], lo) * kPitchA + s0;
+                const int t = tile_row(kLowTile[f], lo), s0 = 32 * kLowStep[f] + 8 * g;
+                const float *src = sA + ((s0 & ~15) + (t & 15)) * kPitchA + (t & ~15) + (s0 & 15);
                 v[0] = *reinterpret_cast<const f32x4 *>(src) *
-                       *reinterpret_cast<const f32x4 *>(sBeta + s0);
+                       *reinterpret_cast<const f32x4 *>(d.beta + s0);
                 v[1] = *reinterpret_cast<const f32x4 *>(src + 4) *
-                       *reinterpret_cast<const f32x4 *>(sBeta + s0 + 4);
+                       *reinterpret_cast<const f32x4 *>(d.beta + s0 + 4);
+                if (s0 / 16 > t / 16) v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
             put_split<E>(rec + f * Rec::kSplitBytes, to_split<E>(v[0], v[1]), lane);
         }
@@ -273,8 +328,7 @@ template <class E, int K, bool BWD>
 hipError_t launch_prep_t(const PrepArgs &a, int slots, hipStream_t stream) {
     constexpr int kLds = prep_lds<E, K>();
     const auto fn = prep_kernel<E, K, BWD>;
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(fn), kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(fn, dim3((unsigned)((size_t)slots * a.Hk)), dim3(256), kLds, stream, a);
     return hipGetLastError();

@@ -63,15 +63,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _token_stride(x, name, B, T, H, C):
-    """Elements from one token's channels to the next's (0: dense)."""
-    if tuple(x.shape) != (B, T, H, C):
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(B, T, H, C)}")
+def _token_stride(x, name, lead, H, C):
+    """Elements from one token's channels to the next's (0: dense) of x [*lead, H, C]."""
+    if x.shape != (*lead, H, C):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(*lead, H, C)}")
     if x.is_contiguous():
         return 0
     s = x.stride()
-    step = s[1] if T > 1 else s[0]
-    if s[3] != 1 or (H > 1 and s[2] != C) or (B > 1 and s[0] != T * step):
+    B, T = lead if len(lead) == 2 else (1, *lead)
+    step = s[-3] if T > 1 else s[0]
+    if s[-1] != 1 or (H > 1 and s[-2] != C) or (B > 1 and s[0] != T * step):
         raise ValueError(f"{name}: the channels of a token must be dense and tokens equally spaced "
                          f"(strides {s})")
     return 0 if B * T == 1 else step
@@ -80,7 +81,7 @@ def _token_stride(x, name, B, T, H, C):
 def _dense(t, name, shape, dtype, device):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -98,62 +99,65 @@ def _index(torch, t, name, n, device):
 
 
 def _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots_out, pool, scale, normalize):
-    """The C problem of checked inputs, the number of sequences and the state shape's tail."""
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q and k are [B,T,Hk,K], v is [B,T,Hv,V]")
-    B, T, Hk, K = q.shape
-    Hv, V = v.shape[2:]
-    dt = q.dtype
-    if dt != torch.bfloat16 and dt != torch.float32:
+    """The C problem of checked inputs, and the shape of one sequence's states.  q [*lead, Hk, K] with
+    lead (B, T), or (B,) for single tokens."""
+    lead, (Hk, K), (Hv, V) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    dt, dev = q.dtype, q.device
+    if dt == torch.bfloat16:
+        code = DT_BF16
+    elif dt == torch.float32:
+        code = DT_F32
+    else:
         raise TypeError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
-    dev = q.device
     if dev.type != "cuda":
         raise ValueError("inputs must live on the GPU")
-    for name, x in (("k", k), ("v", v)):
-        if x.dtype != dt:
-            raise TypeError("all per-token inputs must share one dtype")
-        if x.device != dev:
-            raise ValueError(f"{name} must live on {dev}, not {x.device}")
-    _dense(g, "g", (B, T, Hv), dt, dev)
-    _dense(beta, "beta", (B, T, Hv), dt, dev)
-    p = Problem()
-    p.q_stride = _token_stride(q, "q", B, T, Hk, K)
-    p.k_stride = _token_stride(k, "k", B, T, Hk, K)
-    p.v_stride = _token_stride(v, "v", B, T, Hv, V)
-    n = B
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("all per-token inputs must share one dtype")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"all inputs must live on {dev}")
+    gates = (*lead, Hv)
+    _dense(g, "g", gates, dt, dev)
+    _dense(beta, "beta", gates, dt, dev)
+    n, total = lead[0], lead[0] * lead[1] if len(lead) == 2 else lead[0]
+    cu = None
     if cu_seqlens is not None:
-        if B != 1:
+        if n != 1:
             raise ValueError("a packed batch has B = 1")
         n = cu_seqlens.numel() - 1
         if n < 1:
             raise ValueError("cu_seqlens holds n + 1 offsets of n >= 1 sequences")
-        p.cu_seqlens = _index(torch, cu_seqlens, "cu_seqlens", n + 1, dev)
-    p.n_seq, p.total = n, B * T
-    p.Hk, p.Hv, p.K, p.V = Hk, Hv, K, V
-    p.slots_in = _index(torch, slots_in, "slots_in", n, dev)
-    p.slots_out = _index(torch, slots_out, "slots", n, dev)
-    p.pool = n if pool is None else pool
-    p.scale = K ** -0.5 if scale is None else scale
-    p.normalize = 1 if normalize else 0
-    p.dt = DT_BF16 if dt == torch.bfloat16 else DT_F32
+        cu = _index(torch, cu_seqlens, "cu_seqlens", n + 1, dev)
+    p = Problem(n, total, cu, Hk, Hv, K, V, _token_stride(q, "q", lead, Hk, K),
+                _token_stride(k, "k", lead, Hk, K), _token_stride(v, "v", lead, Hv, V),
+                _index(torch, slots_in, "slots_in", n, dev), _index(torch, slots_out, "slots", n, dev),
+                n if pool is None else pool, K ** -0.5 if scale is None else scale,
+                1 if normalize else 0, code)
     return p, n, (Hv, V, K)
+
+
+def _check_ranks(q, k, v, g, beta):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4 or g.dim() != 3 or beta.dim() != 3:
+        raise ValueError("q and k are [B,T,Hk,K], v is [B,T,Hv,V], g and beta are [B,T,Hv]")
 
 
 class _On:
     """The tensors' device as the current one, and the stream a call goes to."""
 
+    __slots__ = ("torch", "device", "guard", "given", "handle")
+
     def __init__(self, torch, device, stream):
-        if stream is not None and stream.device != device:
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        elif stream.device == device:
+            self.handle = stream.cuda_stream
+        else:
             raise ValueError(f"the stream must be one of {device}, not {stream.device}")
-        self.torch, self.device = torch, device
-        self.guard = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-            self.guard.__enter__()
-        self.given = stream
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        self.torch, self.device, self.given = torch, device, stream
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
     def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
         return self
 
     def __exit__(self, *exc):
@@ -224,6 +228,7 @@ def gated_delta_forward(q, k, v, g, beta, s0=None, *, cu_seqlens=None, slots=Non
         pool = 1 if ref is None else ref.shape[0]
         if slots_in is None:
             slots_in = slots
+    _check_ranks(q, k, v, g, beta)
     p, n, tail = _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots, pool, scale, normalize)
     if slots is not None and s0 is None and s_out is None:
         p.slots_in = p.slots_out = None
@@ -253,13 +258,12 @@ def gated_delta_decode(q, k, v, g, beta, state, *, slots=None, scale=None, norma
     rows with a slot outside the pool are left as they are), is updated in place.  Returns o [B,Hv,V]."""
     import torch
 
-    if q.dim() != 3 or v.dim() != 3 or g.dim() != 2 or beta.dim() != 2:
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or g.dim() != 2 or beta.dim() != 2:
         raise ValueError("q and k are [B,Hk,K], v is [B,Hv,V], g and beta are [B,Hv]")
     if state is None:
         raise ValueError("decode needs the state")
     pool = None if slots is None else state.shape[0]
-    p, _, tail = _problem(torch, q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1),
-                          beta.unsqueeze(1), None, slots, slots, pool, scale, normalize)
+    p, _, tail = _problem(torch, q, k, v, g, beta, None, slots, slots, pool, scale, normalize)
     dev = q.device
     _dense(state, "state", (p.pool, *tail), torch.float32, dev)
     _dense(o, "o", v.shape, q.dtype, dev)
@@ -279,6 +283,7 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
     v), in the inputs' dtype, are what :func:`gated_delta_backward` needs besides the inputs."""
     import torch
 
+    _check_ranks(q, k, v, g, beta)
     p, n, tail = _problem(torch, q, k, v, g, beta, cu_seqlens, None, None, None, scale, normalize)
     dev = q.device
     ref = ctypes.byref(p)
@@ -310,6 +315,7 @@ def gated_delta_backward(q, k, v, g, beta, d_o, s_ckpt, u, ds_T=None, *, cu_seql
     (in place).  Rows of a packed batch outside every sequence are not written."""
     import torch
 
+    _check_ranks(q, k, v, g, beta)
     p, n, tail = _problem(torch, q, k, v, g, beta, cu_seqlens, None, None, None, scale, normalize)
     dev, dt = q.device, q.dtype
     ref = ctypes.byref(p)

@@ -196,10 +196,11 @@ def test_binding_refuses_what_is_not_on_a_gpu_or_has_wrong_shapes():
 
 def test_token_strides():
     base = torch.zeros(2, 5, 7, 64, dtype=torch.bfloat16)
-    assert G._token_stride(base, "q", 2, 5, 7, 64) == 0
-    assert G._token_stride(base[:, :, 2:5], "q", 2, 5, 3, 64) == 7 * 64
-    assert G._token_stride(base[:1, :, :1], "q", 1, 5, 1, 64) == 7 * 64
-    assert G._token_stride(base[:, :1, 2:5], "q", 2, 1, 3, 64) == 5 * 7 * 64
+    assert G._token_stride(base, "q", (2, 5), 7, 64) == 0
+    assert G._token_stride(base[:, :, 2:5], "q", (2, 5), 3, 64) == 7 * 64
+    assert G._token_stride(base[:1, :, :1], "q", (1, 5), 1, 64) == 7 * 64
+    assert G._token_stride(base[:, :1, 2:5], "q", (2, 1), 3, 64) == 5 * 7 * 64
+    assert G._token_stride(base[:, 2], "q", (2,), 7, 64) == 5 * 7 * 64
     for bad in (base[:, :3], base.transpose(1, 2), base[..., ::2]):
         with pytest.raises(ValueError):
-            G._token_stride(bad, "q", *bad.shape)
+            G._token_stride(bad, "q", tuple(bad.shape[:2]), *bad.shape[2:])
