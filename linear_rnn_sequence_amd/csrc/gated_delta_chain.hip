@@ -272,6 +272,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         gk.load(kp + (long long)c * kChunk * p.k_stride, p.k_stride, live, tid);
         if (MODE != kSummary)
             gq.load(qp + (long long)c * kChunk * p.q_stride, p.q_stride, live, tid);
+    };
+    auto fetch_record = [&](int c) {
         const char *r = rec + c * rec_step;
         if constexpr (L::kRecord) {
             const Buffer b(r, c < chunks ? Rec::kBytes : 0);
@@ -316,12 +318,14 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
     };
     if (chunks > 0) {
         fetch_rows(0);
+        fetch_record(0);
         if constexpr (L::kShared) {
             fetch_values(0);
             gv.store(values(0), vtid);
         }
         put_rows(0);
         fetch_rows(1);
+        fetch_record(1);
         fetch_values(L::kShared ? 1 : 0);
         // as many accesses behind these loads as the loop has, so that it waits for no
         // more than it needs
@@ -341,7 +345,7 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         if constexpr (L::kShared) gv.store(values(c + 1), vtid);
         if constexpr (!L::kRecord) fetch_T(c);
         fetch_rows(c + 2);
-        if constexpr (L::kShared) fetch_values(c + 2);
+        if constexpr (!L::kShared) fetch_record(c + 2);
         const char *buf = buffer(c);
         const Tile<E, K> tk{reinterpret_cast<E *>(const_cast<char *>(buf))},
             tq{reinterpret_cast<E *>(const_cast<char *>(buf) + kTile)};
@@ -383,7 +387,13 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
             R[i] = tv.template column4<4>(tile_row(i, 4 * g), vcol, lane) + row_bcast4(kS, i) * X[i];
             if (MODE != kSummary) O[i] *= qs;
         }
+        // (keeps what is read from shared memory for the next products out of the
+        // registers that these need)
         if (MODE != kSummary) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (L::kShared) {  // not all loads at once: 320 workgroups took 317 us, not 340
+            fetch_record(c + 2);
+            fetch_values(c + 2);
+        }
         if constexpr (!L::kRecord && MODE != kSummary) fetch_P(c);
         f32x4 U[4];
 #pragma unroll
@@ -549,13 +559,25 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
 
 constexpr int kValues = 64;  // values of a backward workgroup: 16 a wave
 
-// The same pipeline backwards: the rows of k, q and dO double-buffered, T^T and
-// P^T loaded again as soon as they have been used.
+// Shared memory of a backward workgroup: as the forward's.
+template <class E, int K>
+struct BackwardLds {
+    static constexpr int kTile = tile_bytes<E, K>(kChunk);
+    static constexpr bool kRecord = sizeof(E) == 2;
+    static constexpr int kRecPer = (BwdRecord<E>::kBytes + 16 * kThreads - 1) / (16 * kThreads);
+    static constexpr int kRest = kRecord ? kRecPer * 16 * kThreads : kScalarSpace;
+    static constexpr int kBuffer = 2 * kTile + kRest;
+    static constexpr int kBytes = 2 * kBuffer + tile_bytes<E, kValues>(kChunk);
+    static_assert(kBytes <= 160 * 1024, "fits a CU");
+};
+
+// The same pipeline backwards: the rows of k and q and the record (bf16) double-buffered;
+// float loads T^T and P^T again as soon as they have been used.
 template <class E, int K>
 __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p) {
     using Rec = BwdRecord<E>;
-    constexpr int KS = K / 32, kTile = tile_bytes<E, K>(kChunk);
-    constexpr int kBuffer = 2 * kTile + kScalarSpace;
+    using L = BackwardLds<E, K>;
+    constexpr int KS = K / 32, kTile = L::kTile, kBuffer = L::kBuffer;
     extern __shared__ __align__(16) char lds[];
 
     const int tid = threadIdx.x, lane = tid & 63,
@@ -594,25 +616,39 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
 
     Stage<E, K, kChunk, kThreads> gk, gq;
     Stage<E, 16, kChunk, 64> go;  // this wave's values
-    float gs, last_next;
+    u32x4 gr[L::kRecPer];
+    float gs = 0.f, last_next = 0.f;
     Split<E> T[6], P[6];
     auto record = [&](int c) { return rec + (long long)c * (long long)rec_step; };
     auto fetch_rows = [&](int c) {
         const int live = live_of(c);
         gk.load(kp + (long long)c * kChunk * p.k_stride, p.k_stride, live, tid);
         gq.load(qp + (long long)c * kChunk * p.q_stride, p.q_stride, live, tid);
-        gs = Buffer(record(c) + Rec::kScalars, live > 0 ? kScalarSpace : 0).load_float(tid * 4);
+        if constexpr (L::kRecord) {
+            const Buffer b(record(c), live > 0 ? Rec::kBytes : 0);
+#pragma unroll
+            for (int i = 0; i < L::kRecPer; ++i) gr[i] = b.load16((tid + i * kThreads) * 16);
+        } else {
+            gs = Buffer(record(c) + Rec::kScalars, live > 0 ? kScalarSpace : 0).load_float(tid * 4);
+        }
     };
     auto put_rows = [&](int c) {
         char *b = buffer(c);
         gk.store(Tile<E, K>{reinterpret_cast<E *>(b)}, tid);
         gq.store(Tile<E, K>{reinterpret_cast<E *>(b + kTile)}, tid);
-        reinterpret_cast<float *>(b + 2 * kTile)[tid] = gs;
+        if constexpr (L::kRecord) {
+#pragma unroll
+            for (int i = 0; i < L::kRecPer; ++i)
+                *reinterpret_cast<u32x4 *>(b + 2 * kTile + (tid + i * kThreads) * 16) = gr[i];
+        } else {
+            reinterpret_cast<float *>(b + 2 * kTile)[tid] = gs;
+        }
     };
     auto fetch_values = [&](int c) {
         go.load(dop + (long long)c * kChunk * row, row, live_of(c), lane);
-        last_next =
-            Buffer(record(c) + Rec::kScalars + kScalarSpace, c >= 0 ? 4 : 0).load_float(0);
+        if constexpr (!L::kRecord)
+            last_next =
+                Buffer(record(c) + Rec::kScalars + kScalarSpace, c >= 0 ? 4 : 0).load_float(0);
     };
     auto fetch_T = [&](int c) {
         const char *src = rec + (c > 0 ? c : 0) * rec_step;
@@ -626,11 +662,18 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
     };
     if (chunks > 0) {
         fetch_rows(chunks - 1);
-        fetch_values(chunks - 1);
-        fetch_P(chunks - 1);
-        fetch_T(chunks - 1);
+        if constexpr (!L::kRecord) {
+            fetch_P(chunks - 1);
+            fetch_T(chunks - 1);
+        }
         put_rows(chunks - 1);
         fetch_rows(chunks - 2);
+        fetch_values(chunks - 1);
+        // as many accesses behind these loads as the loop has
+        const Buffer none(dvp, 0);
+#pragma unroll
+        for (int i = 0; i < (K / 32 + 4) * (int)sizeof(E) / 2; ++i)
+            none.store16(0, u32x4{0u, 0u, 0u, 0u});
     }
     for (int c = chunks - 1; c >= 0; --c) {
         const int live = live_of(c);
@@ -639,9 +682,10 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
         fetch_rows(c - 2);
         char *b0 = buffer(c);
         const Tile<E, K> tk{reinterpret_cast<E *>(b0)}, tq{reinterpret_cast<E *>(b0 + kTile)};
-        const Scalars &sc = *reinterpret_cast<const Scalars *>(b0 + 2 * kTile);  // without `last`
+        const char *rc = b0 + 2 * kTile;
+        const Scalars &sc = *reinterpret_cast<const Scalars *>(L::kRecord ? rc + Rec::kScalars : rc);
         go.store(to, lane);
-        const float last = last_next;
+        const float last = L::kRecord ? sc.last : last_next;
         const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)],
                     beta = sc.beta[own_token(lane)];
         fetch_values(c - 1);
@@ -654,9 +698,13 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const Split<E> b = to_split<E>(D.t[2 * ks], D.t[2 * ks + 1]);
+            Frag<E> fk[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                X[i] = mma(tk.rows(tile_row(i, lo), 32 * ks, g), b, X[i]);
+            for (int i = 0; i < 4; ++i) fk[i] = tk.rows(tile_row(i, lo), 32 * ks, g);
+#pragma unroll
+            for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) X[i] = mma_mixed(part, fk[i], b, X[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -664,9 +712,17 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
         Frag<E> fo[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st) fo[st] = to.template cols<4>(32 * st, 0, lane);
+        if constexpr (L::kRecord)
 #pragma unroll
-        for (int f = 0; f < 6; ++f) X[kUpTile[f]] = mma(P[f], fo[kUpStep[f]], X[kUpTile[f]]);
-        fetch_P(c - 1);
+            for (int f = 0; f < 6; ++f)
+                P[f] = get_split<E>(rc + Rec::kP + f * Rec::kSplitBytes, lane);
+#pragma unroll
+        for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+            for (int f = 0; f < 6; ++f)
+                X[kUpTile[f]] = mma_mixed(part, P[f], fo[kUpStep[f]], X[kUpTile[f]]);
+        if constexpr (!L::kRecord) fetch_P(c - 1);
+        __builtin_amdgcn_sched_barrier(0);  // as in the forward
         // dR = T^T dU
         f32x4 R[4];
 #pragma unroll
@@ -674,11 +730,18 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const Split<E> b = to_split<E>(X[2 * st], X[2 * st + 1]);
+            if constexpr (L::kRecord)
 #pragma unroll
-            for (int f = 0; f < 6; ++f)
-                if (kUpStep[f] == st) R[kUpTile[f]] = mma(T[f], b, R[kUpTile[f]]);
+                for (int f = 0; f < 6; ++f)
+                    if (kUpStep[f] == st) T[f] = get_split<E>(rc + f * Rec::kSplitBytes, lane);
+#pragma unroll
+            for (int part = 0; part < kPartsSplit<E>; ++part)
+#pragma unroll
+                for (int f = 0; f < 6; ++f)
+                    if (kUpStep[f] == st)
+                        R[kUpTile[f]] = mma_split(part, T[f], b, R[kUpTile[f]]);
         }
-        fetch_T(c - 1);
+        if constexpr (!L::kRecord) fetch_T(c - 1);
         {
             const Buffer bv(dvp + (long long)c * kChunk * row, row_bytes<E>(live, row)),
                 br(drp + (long long)c * kChunk * row, row_bytes<E>(live, row));
@@ -705,20 +768,32 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
             }
             const Split<E> bo = to_split<E>(x0, x1);
 #pragma unroll
-            for (int m = 0; m < K / 16; ++m) {
-                const int col = 32 * (m >> 1) + 4 * (m & 1);
-                D.t[m] = mma(tk.template cols<8>(32 * st, col, lane), b, D.t[m]);
-                D.t[m] = mma(tq.template cols<8>(32 * st, col, lane), bo, D.t[m]);
+            for (int half = 0; half < K / 64; ++half) {  // four tiles of keys at a time
+                Frag<E> ak[4], aq[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int col = 64 * half + 32 * (m >> 1) + 4 * (m & 1);
+                    ak[m] = tk.template cols<8>(32 * st, col, lane);
+                    aq[m] = tq.template cols<8>(32 * st, col, lane);
+                }
+#pragma unroll
+                for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        f32x4 &d = D.t[4 * half + m];
+                        d = mma_mixed(part, ak[m], b, d);
+                    }
+#pragma unroll
+                for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        f32x4 &d = D.t[4 * half + m];
+                        d = mma_mixed(part, aq[m], bo, d);
+                    }
             }
         }
     }
     if (p.s_out) store_state(D, p.s_out + state_at, g, lo);
-}
-
-// shared memory of a chain workgroup
-template <class E, int K>
-constexpr int chain_lds() {
-    return 2 * (2 * tile_bytes<E, K>(kChunk) + kScalarSpace) + tile_bytes<E, kValues>(kChunk);
 }
 
 template <class F>
@@ -752,7 +827,7 @@ hipError_t launch_forward_t(const ChainArgs &a, bool train, int units, int n_seq
 template <class E, int K>
 hipError_t launch_backward_t(const ChainArgs &a, int n_seq, hipStream_t stream) {
     return launch(backward_chain_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / kValues),
-                  kThreads, chain_lds<E, K>(), a, stream);
+                  kThreads, BackwardLds<E, K>::kBytes, a, stream);
 }
 
 ChainArgs chain_args(const Problem &p) {
