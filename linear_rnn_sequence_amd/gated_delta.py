@@ -147,7 +147,9 @@ class _On:
 
     def __init__(self, torch, device, stream):
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            # the handle of torch.cuda.current_stream(device), without the object around it: 1.8 us of a
+            # single token's 14
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
         elif stream.device == device:
             self.handle = stream.cuda_stream
         else:
@@ -171,6 +173,12 @@ class _On:
         if self.given is not None:
             t.record_stream(self.given)
         return t
+
+    def like(self, x):
+        """Dense memory of x's shape and type."""
+        if self.given is not None or not x.is_contiguous():
+            return self.empty(x.shape, x.dtype)
+        return self.torch.empty_like(x)
 
     def workspace(self, need, given):
         if given is None:
@@ -240,7 +248,7 @@ def gated_delta_forward(q, k, v, g, beta, s0=None, *, cu_seqlens=None, slots=Non
     _dense(o, "o", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
         if o is None:
-            o = on.empty(v.shape, q.dtype)
+            o = on.like(v)
         if s_out is None and want_state:
             s_out = on.empty(states, torch.float32)
         ref = ctypes.byref(p)
@@ -269,7 +277,7 @@ def gated_delta_decode(q, k, v, g, beta, state, *, slots=None, scale=None, norma
     _dense(o, "o", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
         if o is None:
-            o = on.empty(v.shape, q.dtype)
+            o = on.like(v)
         _check(lib().gated_delta_decode(
             ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(o),
             on.handle), "gated_delta_decode")
@@ -294,8 +302,8 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
     _dense(s_ckpt, "s_ckpt", (chunks, *tail), q.dtype, dev)
     _dense(u, "u", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
-        o = on.empty(v.shape, q.dtype) if o is None else o
-        u = on.empty(v.shape, q.dtype) if u is None else u
+        o = on.like(v) if o is None else o
+        u = on.like(v) if u is None else u
         s_ckpt = on.empty((chunks, *tail), q.dtype) if s_ckpt is None else s_ckpt
         if s_out is None and want_state:
             s_out = on.empty((n, *tail), torch.float32)
