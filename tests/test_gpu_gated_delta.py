@@ -526,3 +526,115 @@ def test_long_sequences_of_few_heads(rnn, layout):
         close_state(pool[i], f64(S[0]), dtype)
         if n:
             close(o[:, a:a + n], f64(torch.cat(parts, 1)), dtype, f"o of sequence {i}")
+
+
+# (dtype, K, V, Hk, Hv)
+@pytest.mark.parametrize("layout", [("bf16", 64, 128, 1, 2), ("bf16", 128, 128, 1, 2), ("bf16", 128, 256, 1, 3),
+                                    ("bf16", 64, 64, 2, 2), ("f32", 64, 64, 1, 3), ("f32", 128, 128, 1, 2)], ids=str)
+def test_many_ragged_sequences(rnn, layout):
+    """More sequences than CUs, whose states lie in a pool in another order: the workgroups of the most
+    waves, and one workgroup for all value heads of a key head.  Every tenth sequence against float64."""
+    dtype, K, V, Hk, Hv = layout
+    n = 300
+    r = np.random.default_rng(5)
+    lens = r.integers(0, 150, n)
+    lens[[0, 10, 20, 30, 40]] = [0, 1, 64, 149, 128]
+    cu, total = np.cumsum([0, *lens]), int(lens.sum())
+    x = inputs(total, Hk, Hv, K, V, dtype, 71)
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    order = r.permutation(n + 4)[:n]
+    old = states(n + 4, Hv, V, K, 6)
+    pool = old.clone()
+    o, _ = rnn.gated_delta_forward(*x.values(), s0=pool, s_out=pool, cu_seqlens=cut, normalize=True,
+                                   slots=torch.tensor(order, dtype=torch.int32, device="cuda"))
+    s0 = old[torch.from_numpy(order).cuda()].contiguous()
+    ot, st, ck, u = rnn.gated_delta_forward_train(*x.values(), s0=s0, cu_seqlens=cut, normalize=True)
+    d_o, ds = torch.randn(1, total, Hv, V, device="cuda").to(DT[dtype]), states(n, Hv, V, K, 7)
+    grads = rnn.gated_delta_backward(*x.values(), d_o, ck, u, ds_T=ds, cu_seqlens=cut, normalize=True)
+    spare = sorted(set(range(n + 4)) - set(order.tolist()))
+    assert torch.equal(pool[spare], old[spare])
+    for i in range(0, n, 10):
+        a, b = cu[i], cu[i + 1]
+        want, S, _ = gd.forward(*rows(x, 0, a, b), f64(s0[i]), normalize=True)
+        ref = gd.backward(*rows(x, 0, a, b), f64(d_o[0, a:b]), f64(ds[i]), f64(s0[i]), normalize=True)
+        for y, z in ((o, pool[order[i]]), (ot, st[i])):
+            close(y[0, a:b], want, dtype, f"o of sequence {i}")
+            close_state(z, S, dtype, f"state of sequence {i}")
+        for name, got, w in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, ref):
+            close(got[0, a:b], w, dtype, f"{name} of sequence {i}")
+        close_state(grads[5][i], ref[5], dtype, f"ds0 of sequence {i}")
+
+
+@pytest.mark.parametrize("layout", [("bf16", 64, 128, 1, 1), ("bf16", 128, 128, 1, 2), ("f32", 64, 64, 1, 2),
+                                    ("f32", 128, 128, 1, 1)], ids=str)
+@pytest.mark.parametrize("T", [1024, 1087, 2049])
+def test_segments_against_float64(rnn, layout, T):
+    """One sequence that is done in segments, whole and as the second of a graph's two replays."""
+    dtype, K, V, Hk, Hv = layout
+    x = inputs(T, Hk, Hv, K, V, dtype, 80 + T, slow=True)
+    s0 = states(1, Hv, V, K, 8)
+    need = rnn.gated_delta_forward_workspace_bytes
+    # more workspace than the chunks need
+    assert need(T, Hk, Hv, K, V, dtype=dtype) > need(64, 1, 1, K, V, dtype=dtype) * Hv * ((T + 63) // 64)
+    o, s = rnn.gated_delta_forward(*x.values(), s0=s0, normalize=True)
+    want, S, _ = gd.forward(*rows(x, 0, 0, T), f64(s0[0]), normalize=True)
+    close(o[0], want, dtype, "o")
+    close_state(s[0], S, dtype)
+    work = torch.empty(need(T, Hk, Hv, K, V, dtype=dtype), dtype=torch.uint8, device="cuda")
+    o2, s2 = torch.empty_like(o), torch.empty_like(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rnn.gated_delta_forward(*x.values(), s0=s0, normalize=True, o=o2, s_out=s2, workspace=work)
+    for _ in range(3):
+        work.fill_(255)  # what a call finds in its workspace does not matter (NaN here)
+        o2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(s, s2)
+
+
+def test_offsets_behind_32_bits(rnn):
+    """A pool of 2.1e9 elements: prefill and decode at its end, and moves from end to end.  Then a batch
+    whose values, records and chunk states lie behind 2^31 elements or 2^32 bytes, training included."""
+    Hk, Hv, K, V = 1, 8, 128, 128
+    slots = 2 ** 31 // (Hv * V * K) + 3
+    pool = torch.empty(slots, Hv, V, K, device="cuda")
+    last = torch.tensor([slots - 1], dtype=torch.int32, device="cuda")
+    start = states(1, Hv, V, K, 1)
+    pool[-1] = start[0]
+    x = inputs(70, Hk, Hv, K, V, "bf16", 99)
+    o, s = rnn.gated_delta_forward(*x.values(), s0=start, normalize=True)
+    op, _ = rnn.gated_delta_forward(*x.values(), s0=pool, s_out=pool, slots=last, normalize=True)
+    assert torch.equal(o, op) and torch.equal(s[0], pool[-1])
+    one = [a[:, 0].contiguous() for a in x.values()]
+    a, b = rnn.gated_delta_decode(*one, s, normalize=True), rnn.gated_delta_decode(*one, pool, slots=last,
+                                                                                  normalize=True)
+    assert torch.equal(a, b) and torch.equal(s[0], pool[-1])
+    pool[0] = 1.0
+    rnn.state_move(pool, torch.tensor([slots - 1, 0], dtype=torch.int32, device="cuda"),
+                   torch.tensor([0, slots - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(s[0], pool[0]) and (pool[-1] == 1).all()
+    del pool
+
+    Hk, Hv, K, V = 1, 64, 64, 128
+    T, short = 2 ** 31 // (Hv * V) + 64, 70
+    total = T + short
+    dt = torch.bfloat16
+    g = torch.Generator("cuda").manual_seed(3)
+    new = lambda *shape: torch.randn(shape, device="cuda", dtype=dt, generator=g)  # noqa: E731
+    x = [new(1, total, Hk, K), new(1, total, Hk, K), new(1, total, Hv, V), -new(1, total, Hv).abs(),
+         new(1, total, Hv).sigmoid()]
+    cu = torch.tensor([0, T, total], dtype=torch.int32, device="cuda")
+    d_o = new(1, total, Hv, V)
+    o, s, ck, u = rnn.gated_delta_forward_train(*x, cu_seqlens=cu, normalize=True)
+    grads = rnn.gated_delta_backward(*x, d_o, ck, u, cu_seqlens=cu, normalize=True)
+    tail = [t[:, T:].contiguous() for t in x]
+    to, ts, tck, tu = rnn.gated_delta_forward_train(*tail, normalize=True)
+    want = rnn.gated_delta_backward(*tail, d_o[:, T:].contiguous(), tck, tu, normalize=True)
+    close(o[:, T:], f64(to), "bf16", "o")
+    close_state(s[1], f64(ts[0]), "bf16")
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, want):
+        close(a[:, T:], f64(b), "bf16", name)
+    close_state(grads[5][1], f64(want[5][0]), "bf16", "ds0")
+    plain, _ = rnn.gated_delta_forward(*x, cu_seqlens=cu, normalize=True, want_state=False)
+    assert torch.equal(plain[:, T - 200:], o[:, T - 200:])
