@@ -121,15 +121,15 @@ __device__ __forceinline__ Place place_of(unsigned block, int Hk, int Hv, int pa
 enum Mode { kInfer, kTrain, kSummary };
 
 // Shared memory of a forward workgroup of W waves: two buffers with a chunk's k and q
-// rows and its record (bf16) or the record's scalars (float), and each wave's
-// values.  kSummary has no use for q and P.  In bf16 with 128 keys and eight waves that
+// rows and its record (float with 128 keys has room for the record's scalars only),
+// and the values.  kSummary has no use for q and P.  In bf16 with 128 keys and eight waves that
 // leaves 80 KB of 128, so that a CU has two workgroups, which take turns at waiting: 448
 // of them took 328 us, and 367 us one at a time.
 template <class E, int K, int W, Mode MODE>
 struct ForwardLds {
     static constexpr int kThreads = 64 * W;
     static constexpr int kTile = tile_bytes<E, K>(kChunk);
-    static constexpr bool kRecord = sizeof(E) == 2;
+    static constexpr bool kRecord = sizeof(E) == 2 || K == 64;
     // a record's bytes behind those left out, and where its parts lie in shared memory
     static constexpr int kPBytes = MODE == kSummary ? FwdRecord<E>::kScalars - FwdRecord<E>::kP : 0;
     static constexpr int kScalarsAt = FwdRecord<E>::kScalars - kPBytes;
@@ -143,8 +143,8 @@ struct ForwardLds {
     // wave's 16 values are pieces of 32 bytes, but pass through shared memory twice more:
     // with 64 keys, where memory is what a chunk waits for, 320 workgroups took
     // 345 us with them and 375 us without; with 128 keys, where shared memory is the
-    // busier, 256 took 307 us with them and 278 us without.  float has no room.
-    static constexpr bool kShared = kRecord && MODE != kSummary && K == 64;
+    // busier, 256 took 307 us with them and 278 us without.  In float a piece has 64 bytes.
+    static constexpr bool kShared = sizeof(E) == 2 && MODE != kSummary && K == 64;
     static constexpr int kValueCols = kShared ? 16 * W : 16;
     static constexpr int kValueTile = tile_bytes<E, kValueCols>(kChunk);
     static constexpr int kBytes = 2 * kBuffer + (kShared ? 2 : W) * kValueTile;
@@ -154,19 +154,28 @@ struct ForwardLds {
 
 // The chunks' shared rows are double-buffered in shared memory: while the waves work
 // on chunk c, the rows of c + 1 go from registers to the other buffer and those
-// of c + 2 are on their way to the registers.  In bf16 the chunk's record (T, P
-// and scalars) goes the same way; waves that each loaded T and P for themselves
-// kept the CU's vector cache busy longer than its matrix cores.  In float the
-// record does not fit, and the products take so long that the loads do not
-// matter.  So a load has about one chunk's time to arrive, and a chunk needs one
-// barrier.  Loads of chunks behind the last one are buffer accesses out of range.
+// of c + 2 are on their way to the registers.  The chunk's record (T, P and scalars)
+// goes the same way: waves that each loaded T and P for themselves kept the CU's
+// vector cache busy longer than its matrix cores (where it does not fit, float with
+// 128 keys, they still do).  So a load has about one chunk's time to arrive, and
+// a chunk needs one barrier.  Loads of chunks behind the last one are buffer
+// accesses out of range.
+//
+// What bounds it: a chunk of 128 keys and 128 values (eight waves, one workgroup per
+// CU) takes about 8000 cycles, of which shared memory is busy 4400, a SIMD's matrix
+// core 3300 and its vector units 3100; the products depend on each other, and two
+// waves per SIMD, of 256 registers each, do not overlap them fully.  16 sequences of
+// up to 2049 tokens and 32 heads take 138 us, as long as the longest one's chunks
+// one after the other.  With 64 keys and values (8 x 4096 tokens, 40 heads: 317 us)
+// it is memory: 1.07 GB with the records, 3.4 TB/s, at most one chunk ahead.
 //
 // A workgroup takes a whole sequence, or one segment of it (p.seg): kSummary only
 // carries the state over a segment, from zeros (from the sequence's state for its
 // first one), for p.V / (16 W) parts; the parts behind those start from the
 // rows of the unit matrix and see no values, which gives the segment's
 // transition S0 -> S0 M.  combine_kernel turns these into the states at the
-// segments' starts, from which the segments are then done in parallel.
+// segments' starts, from which the segments are then done in parallel (32768 tokens, 32
+// heads of 128 x 128, eight segments: 321, 28 and 268 us).
 template <class E, int K, int W, Mode MODE>
 __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_kernel(
     ChainArgs p) {
@@ -502,7 +511,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
 // From the segments' summaries to the states at their ends, in place: the state
 // left by segment j - 1 times the transition of segment j, plus what segment j
 // leaves from zeros.  One workgroup per sequence, value head and 64 values, a wave
-// per 16; the next transition is loaded while this one is multiplied.
+// per 16; the next transition is loaded while this one is multiplied.  A step's 64 KB
+// (128 keys) take 4 us, the time a CU needs to load them.
 constexpr int kThreads = 256;  // of the kernels below: four waves
 
 template <class E, int K>
@@ -559,11 +569,12 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
 
 constexpr int kValues = 64;  // values of a backward workgroup: 16 a wave
 
-// Shared memory of a backward workgroup: as the forward's.
+// Shared memory of a backward workgroup: as the forward's, always four waves (256
+// workgroups for four sequences of 32 heads of 128 values).
 template <class E, int K>
 struct BackwardLds {
     static constexpr int kTile = tile_bytes<E, K>(kChunk);
-    static constexpr bool kRecord = sizeof(E) == 2;
+    static constexpr bool kRecord = sizeof(E) == 2 || K == 64;
     static constexpr int kRecPer = (BwdRecord<E>::kBytes + 16 * kThreads - 1) / (16 * kThreads);
     static constexpr int kRest = kRecord ? kRecPer * 16 * kThreads : kScalarSpace;
     static constexpr int kBuffer = 2 * kTile + kRest;
@@ -571,8 +582,11 @@ struct BackwardLds {
     static_assert(kBytes <= 160 * 1024, "fits a CU");
 };
 
-// The same pipeline backwards: the rows of k and q and the record (bf16) double-buffered;
-// float loads T^T and P^T again as soon as they have been used.
+// The same pipeline backwards: the rows of k and q and the record double-buffered; where
+// that does not fit (float, 128 keys) T^T and P^T are loaded again as soon as they have been
+// used.  It is bound by the length of the chain of products, one wave per SIMD: 4 x 2048
+// tokens, 32 heads of 128 x 128, take 151 us, 4.7 us a chunk, where the matrix cores are
+// busy 1 us; 177 us before the parts of split products were interleaved (mma_mixed).
 template <class E, int K>
 __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p) {
     using Rec = BwdRecord<E>;

@@ -9,7 +9,9 @@
 // Lane (c, r) of a row's K / 4 lanes owns key columns 4c .. 4c + 3 of four value
 // rows: every state load instruction of a wave reads whole rows (16 bytes per
 // lane), and row sums are DPP reductions.  State accesses are non-temporal,
-// each state is touched once per call.
+// each state is touched once per call.  256 sequences of 32 heads of 128 x 128 move
+// 1.08 GB in 177 us, 6.1 TB/s, where a large copy reaches 6.6 TB/s; one sequence takes
+// 4 us, and the call 12 us of the host.
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
