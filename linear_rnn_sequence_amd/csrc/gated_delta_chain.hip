@@ -20,7 +20,9 @@
 //
 // The state is float32 and what is added to it keeps 16 bits of significand or
 // more (split operands, gated_delta_device.h), so that s_out and ds0 are
-// float32 results; o is rounded to its type and takes S0 and U rounded to it.
+// float32 results; o is rounded to its type and takes U and P rounded to it, which together
+// make its error 1.6 times that of its own rounding.  (U split as well: 1.35 times, but 7%
+// of the kernel's time, for the split's vector instructions; S0 split costs nothing measurable.)
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
@@ -388,7 +390,9 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
                 for (int i = 0; i < 4; ++i) X[i] = mma_mixed(part, fk[i], b, X[i]);
             if (MODE != kSummary)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) O[i] = mma(b.hi, fq[i], O[i]);
+                for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[i] = mma_mixed(part, b, fq[i], O[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
