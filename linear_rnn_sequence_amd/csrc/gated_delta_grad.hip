@@ -33,11 +33,12 @@
 // their way to registers while one is multiplied.
 //
 // What bounds it: 4 x 2048 tokens, 16 key heads of two value heads, 128 x 128 (2048
-// workgroups, one at a time on a CU) take 312 us, 85000 cycles a workgroup: 24000 of them
-// waiting for the first loads and the steps' (the bytes alone are 105 us), 16000 in the
-// steps' products, 21000 in the triangles and the products with k and q (half of it vector
-// instructions), 14000 in the sums for dg.  Shared memory (147 KB) and registers (128 of 16
-// waves) leave no room for a second workgroup, which would fill the waits.
+// workgroups, one at a time on a CU) take 283 us, 76000 cycles a workgroup: 23000 of them
+// waiting for the first loads and the steps' (the bytes alone are 105 us), 14000 in the
+// steps' products, 17000 in the triangles and the products with k and q (half of it vector
+// instructions), 9000 in the sums for dg.  Shared memory (147 KB) and registers (128 of 16
+// waves) leave no room for a second workgroup, which would fill the waits, nor for loads
+// one step further ahead (spilled registers: 408 us).
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
@@ -242,8 +243,11 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
                                tb = part == 0 ? to : part == 1 ? tr : tu;
 #pragma unroll
             for (int x = 0; x < kVt; x += 32) {
+                // (this and the one below keep the operands of only one group of products in
+                // registers: 315 us without them, which spilled others)
+                __builtin_amdgcn_sched_barrier(0);
                 const Frag<E> fo = to.rows(mine, x, g), fr = tr.rows(mine, x, g),
-                              fu = tu.rows(mine, x, g), fb = tb.rows(mine, x, g);
+                              fu = tu.rows(mine, x, g);
                 Frag<E> as[NK], ad[NK], a[4];
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
@@ -251,13 +255,15 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
                     ad[n] = td.template cols<4>(x, key0 + 16 * n, lane);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = ta.rows(tile_row(i, lo), x, g);
-#pragma unroll
                 for (int n = 0; n < NK; ++n) {
                     oS[n] = mma(as[n], fo, oS[n]);
                     rS[n] = mma(as[n], fr, rS[n]);
                     uD[n] = mma(ad[n], fu, uD[n]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                const Frag<E> fb = tb.rows(mine, x, g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = ta.rows(tile_row(i, lo), x, g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) P[i] = mma(a[i], fb, P[i]);
             }
