@@ -26,8 +26,8 @@
 // to the end of its block of 16 and from there to t (both at most 1), of which
 // there are few: a table per value head, with the other factors of t and of s in it
 // (32768 tokens, 16 key heads of two value heads, K = 128: 165 us without the tables, 141 us
-// with them, 4.2 TB/s of rows and records; 8 x 4096 tokens of 40 heads, K = 64: 200 us).
-// Four workgroups a CU: with the registers for five, 300 us in place of those 200.
+// with them, 4.2 TB/s of rows and records; 8 x 4096 tokens of 40 heads, K = 64: 196 us).
+// Four workgroups a CU: with the registers for five, 300 us in place of those 196.
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
@@ -142,15 +142,13 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
             }
         }
         d.from[lane] = c * rk;
-        if (r < r1) {
-            Scalars *sc = reinterpret_cast<Scalars *>(
-                p.records + ((size_t)slot * p.Hv + hk * rep + r) * Rec::kBytes + Rec::kScalars);
-            sc->beta[lane] = strength;
-            sc->kS[lane] = -(BWD ? strength : 1.f) * from0 * rk;
-            sc->kD[lane] = decay(end[3], G) * rk;
-            sc->qS[lane] = from0 * rq;
-            if (lane == 63) sc->last = from0;
-        }
+        Scalars *sc = reinterpret_cast<Scalars *>(
+            p.records + ((size_t)slot * p.Hv + hk * rep + r) * Rec::kBytes + Rec::kScalars);
+        sc->beta[lane] = strength;
+        sc->kS[lane] = -(BWD ? strength : 1.f) * from0 * rk;
+        sc->kD[lane] = decay(end[3], G) * rk;
+        sc->qS[lane] = from0 * rq;
+        if (lane == 63) sc->last = from0;
     };
     if (wave >= 2) load_gates(r0 + wave - 2);
     {
@@ -163,13 +161,15 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
         sqv.store(tq, tid);
     }
     __syncthreads();
-    {
-        const float a = reciprocal_norm(tk, p.normalize, live, tid);
-        const float b = reciprocal_norm(tq, p.normalize, live, tid);
+    if (p.normalize) {
+        const float a = reciprocal_norm(tk, true, live, tid);
+        const float b = reciprocal_norm(tq, true, live, tid);
         if ((tid & 3) == 0) {
             sRk[tid >> 2] = a;
             sRq[tid >> 2] = b;
         }
+    } else if (tid < kChunk) {
+        sRk[tid] = sRq[tid] = tid < live ? 1.f : 0.f;
     }
     // kk: k.k, rows 16 wave + 4g + e, columns 16 j + lo, j <= wave.  qk: q.k with the
     // tokens 16 pt + lo as columns and s = 16 j + 4g + e as rows, j <= pt, or (backward)
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256, 4) void prep_kernel(PrepArgs p) {
         char *rec = p.records + ((size_t)slot * p.Hv + hv) * Rec::kBytes;
         if (r > r0) __syncthreads();  // the last head's reads of sA and of its table
         if ((r - r0) % kHeads == 0) {
-            if (wave >= 2) {
+            if (wave >= 2 && r + wave - 2 < r1) {
                 if (r > r0) load_gates(r + wave - 2);
                 make_table(r + wave - 2);
             }
