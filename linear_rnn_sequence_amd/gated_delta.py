@@ -72,10 +72,12 @@ def _token_stride(x, name, lead, H, C):
     s = x.stride()
     B, T = lead if len(lead) == 2 else (1, *lead)
     step = s[-3] if T > 1 else s[0]
-    if s[-1] != 1 or (H > 1 and s[-2] != C) or (B > 1 and s[0] != T * step):
-        raise ValueError(f"{name}: the channels of a token must be dense and tokens equally spaced "
-                         f"(strides {s})")
-    return 0 if B * T == 1 else step
+    if B * T <= 1:
+        step = H * C
+    if s[-1] != 1 or (H > 1 and s[-2] != C) or (B > 1 and s[0] != T * step) or step < H * C:
+        raise ValueError(f"{name}: the channels of a token must be dense and tokens equally spaced, "
+                         f"none in another's place (strides {s})")
+    return step
 
 
 def _dense(t, name, shape, dtype, device):

@@ -204,3 +204,18 @@ def test_token_strides():
     for bad in (base[:, :3], base.transpose(1, 2), base[..., ::2]):
         with pytest.raises(ValueError):
             G._token_stride(bad, "q", tuple(bad.shape[:2]), *bad.shape[2:])
+
+
+def test_tokens_in_each_others_place_are_refused():
+    """One token shown as several (a stride of nothing, which the library takes for dense rows), and
+    windows that overlap."""
+    one = torch.zeros(1, 1, 7, 64, dtype=torch.bfloat16)
+    flat = torch.zeros(4096, dtype=torch.bfloat16)
+    for bad in (one.expand(1, 5, 7, 64), one.expand(2, 5, 7, 64), flat.as_strided((1, 5, 7, 64), (4096, 64, 64, 1))):
+        with pytest.raises(ValueError):
+            G._token_stride(bad, "q", tuple(bad.shape[:2]), *bad.shape[2:])
+    for bad in (one[0].expand(5, 7, 64), flat.as_strided((5, 7, 64), (64, 64, 1))):
+        with pytest.raises(ValueError):
+            G._token_stride(bad, "q", (5,), 7, 64)
+    assert G._token_stride(one[..., :3, :], "q", (1, 1), 3, 64) in (0, 3 * 64)
+    assert G._token_stride(one[:0], "q", (0, 1), 7, 64) in (0, 7 * 64)
