@@ -29,9 +29,10 @@
  *    [n_seq * T]) or packed (cu_seqlens: n_seq + 1 non-decreasing int32 token
  *    offsets on the device; sequence i has the rows cu_seqlens[i] ..
  *    cu_seqlens[i + 1] - 1 of `total`).  Lengths may be 0 and 1.  Rows outside
- *    every sequence are neither read nor written.  The offsets cannot be checked on the host: the kernels
- *    clamp them to [0, total] and to non-negative lengths, so that wrong ones
- *    give wrong results but no access outside a buffer.
+ *    every sequence are neither read nor written.  The offsets cannot be checked
+ *    on the host: the kernels clamp them to [0, total] and to non-negative
+ *    lengths, so that wrong ones give wrong results but no access outside a
+ *    buffer.
  *  - q, k, v may be strided from token to token (a slice of a joint projection);
  *    the channels of one token are dense [heads, K or V].
  *  - States s0, s_out are float32 [pool, Hv, V, K].  Without slots, sequence i
@@ -44,6 +45,11 @@
  *  - Numerics: float32 sums, states and norms; exp(g) with g below -200 is 0.
  *    Outputs are rounded once to dt.  The states are float32 results also from
  *    bf16 inputs: what is added to them has 16 bits of significand or more.
+ *    The same call gives the same bits.  Few long sequences are computed in
+ *    segments, whose length depends on the sequences and heads of the call, so a
+ *    long sequence's last bits may depend on what else the call holds.
+ *  - A workspace serves one call at a time: calls, or captured graphs, that may run
+ *    at once need one each.  What it held before does not matter.
  *  - Non-finite inputs propagate within a (sequence, value head) pair, and from
  *    q and k to all value heads of their key head; tokens of the same 64-token
  *    chunk before the non-finite one may become non-finite too, earlier chunks

@@ -177,7 +177,7 @@ struct ForwardLds {
 // rows of the unit matrix and see no values, which gives the segment's
 // transition S0 -> S0 M.  combine_kernel turns these into the states at the
 // segments' starts, from which the segments are then done in parallel (32768 tokens, 32
-// heads of 128 x 128, eight segments: 321, 28 and 268 us).
+// heads of 128 x 128, eight segments: 330, 25 and 272 us).
 template <class E, int K, int W, Mode MODE>
 __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_kernel(
     ChainArgs p) {
@@ -515,9 +515,10 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
 // From the segments' summaries to the states at their ends, in place: the state
 // left by segment j - 1 times the transition of segment j, plus what segment j
 // leaves from zeros.  One workgroup per sequence, value head and 64 values, a wave
-// per 16; the next transition is loaded while this one is multiplied.  A step's 64 KB
-// (128 keys) take 4 us, the time a CU needs to load them.
-constexpr int kThreads = 256;  // of the kernels below: four waves
+// per 16 (eight waves, half as many workgroups: 33 us for 25); the next transition is
+// loaded while this one is multiplied.  A step of 128 keys takes 4 us, most of them
+// for the 64 KB of the transition.
+constexpr int kThreads = 256, kValues = 64;  // of the kernels below: four waves of 16 values
 
 template <class E, int K>
 __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
@@ -525,13 +526,13 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63,
               wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
-    const Place at = place_of(blockIdx.x, p.Hk, p.Hv, p.V / 64);
+    const Place at = place_of(blockIdx.x, p.Hk, p.Hv, p.V / kValues);
     const Seq sq = p.lay.seq(at.unit, p.seg);
     const int segments = (sq.end - sq.begin + p.seg - 1) / p.seg;
     if (segments < 3) return;  // the first segment's summary is the second's state already
     const size_t state_size = (size_t)p.V * K;
     float *state = p.seg_state + ((size_t)sq.slot0 * p.Hv + at.hv) * state_size +
-                   (size_t)(at.part * 64 + wave * 16) * K;
+                   (size_t)(at.part * kValues + wave * 16) * K;
     const E *step = static_cast<const E *>(p.seg_step) +
                     ((size_t)sq.slot0 * p.Hv + at.hv) * (kPlanes * K * K);
     const Tile<E, K> tm[2] = {Tile<E, K>{reinterpret_cast<E *>(lds)},
@@ -558,12 +559,19 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
         for (int ks = 0; ks < K / 32; ++ks) {
             const Split<E> b = to_split<E>(S.t[2 * ks], S.t[2 * ks + 1]);
 #pragma unroll
-            for (int m = 0; m < K / 16; ++m) {
-                const int col = 32 * (m >> 1) + 4 * (m & 1);
-                Split<E> a;
-                a.hi = tm[0].template cols<8>(32 * ks, col, lane);
-                if constexpr (kPlanes == 2) a.lo = tm[1].template cols<8>(32 * ks, col, lane);
-                R.t[m] = mma(a, b, R.t[m]);
+            for (int half = 0; half < K / 64; ++half) {  // four tiles of keys at a time
+                Split<E> a[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int col = 64 * half + 32 * (m >> 1) + 4 * (m & 1);
+                    a[m].hi = tm[0].template cols<8>(32 * ks, col, lane);
+                    if constexpr (kPlanes == 2) a[m].lo = tm[1].template cols<8>(32 * ks, col, lane);
+                }
+#pragma unroll
+                for (int part = 0; part < kPartsSplit<E>; ++part)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        R.t[4 * half + m] = mma_split(part, a[m], b, R.t[4 * half + m]);
             }
         }
         S = R;
@@ -571,10 +579,8 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
     }
 }
 
-constexpr int kValues = 64;  // values of a backward workgroup: 16 a wave
-
-// Shared memory of a backward workgroup: as the forward's, always four waves (256
-// workgroups for four sequences of 32 heads of 128 values).
+// Shared memory of a backward workgroup: as the forward's (four waves: 256 workgroups for
+// four sequences of 32 heads of 128 values).
 template <class E, int K>
 struct BackwardLds {
     static constexpr int kTile = tile_bytes<E, K>(kChunk);
@@ -830,9 +836,9 @@ hipError_t launch_forward_t(const ChainArgs &a, bool train, int units, int n_seq
     if (a.seg) {
         hipError_t e = launch(forward_chain_kernel<E, K, W, kSummary>,
                               (size_t)units * a.Hv * (parts + step_parts), 64 * W,
-                      ForwardLds<E, K, W, kSummary>::kBytes, a, stream);
+                              ForwardLds<E, K, W, kSummary>::kBytes, a, stream);
         if (e != hipSuccess) return e;
-        e = launch(combine_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / 64), kThreads,
+        e = launch(combine_kernel<E, K>, (size_t)n_seq * a.Hv * (a.V / kValues), kThreads,
                    (sizeof(E) == 2 ? 2 : 1) * tile_bytes<E, K>(K), a, stream);
         if (e != hipSuccess) return e;
     }
