@@ -21,8 +21,9 @@
 // The state is float32 and what is added to it keeps 16 bits of significand or
 // more (split operands, gated_delta_device.h), so that s_out and ds0 are
 // float32 results; o is rounded to its type and takes U and P rounded to it, which together
-// make its error 1.6 times that of its own rounding.  (U split as well: 1.35 times, but 7%
-// of the kernel's time, for the split's vector instructions; S0 split costs nothing measurable.)
+// make its error 1.6 times that of its own rounding.  (S0 rounded as well: 1.7 times for
+// 1% of a long prefill's time; U split as well: 1.35 times, but 2% more, for the split's
+// vector instructions.)
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 

@@ -369,7 +369,7 @@ def state_move(pool, src, dst, *, slot_dim=0, stream=None):
     if dev.type != "cuda":
         raise ValueError("the pool must live on the GPU")
     layers = pool.shape[0] if slot_dim else 1
-    if layers < 1 or not (pool[0] if slot_dim else pool).is_contiguous():
+    if layers < 1 or not (pool.is_contiguous() or (slot_dim and pool[0].is_contiguous())):
         raise ValueError("each layer's slots must be contiguous")
     slots = pool.shape[slot_dim]
     size = pool.element_size()
