@@ -65,8 +65,9 @@ def _ptr(t):
 
 def _token_stride(x, name, lead, H, C):
     """Elements from one token's channels to the next's (0: dense) of x [*lead, H, C]."""
-    if x.shape != (*lead, H, C):
-        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(*lead, H, C)}")
+    shape = (*lead, H, C)
+    if x.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {shape}")
     if x.is_contiguous():
         return 0
     s = x.stride()
@@ -103,7 +104,8 @@ def _index(torch, t, name, n, device):
 def _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots_out, pool, scale, normalize):
     """The C problem of checked inputs, and the shape of one sequence's states.  q [*lead, Hk, K] with
     lead (B, T), or (B,) for single tokens."""
-    lead, (Hk, K), (Hv, V) = q.shape[:-2], q.shape[-2:], v.shape[-2:]
+    *lead, Hk, K = q.shape
+    Hv, V = v.shape[-2:]
     dt, dev = q.dtype, q.device
     if dt == torch.bfloat16:
         code = DT_BF16
@@ -120,7 +122,8 @@ def _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots_out, pool, sca
     gates = (*lead, Hv)
     _dense(g, "g", gates, dt, dev)
     _dense(beta, "beta", gates, dt, dev)
-    n, total = lead[0], lead[0] * lead[1] if len(lead) == 2 else lead[0]
+    n = lead[0]
+    total = n * lead[1] if len(lead) == 2 else n
     cu = None
     if cu_seqlens is not None:
         if n != 1:
@@ -129,9 +132,10 @@ def _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots_out, pool, sca
         if n < 1:
             raise ValueError("cu_seqlens holds n + 1 offsets of n >= 1 sequences")
         cu = _index(torch, cu_seqlens, "cu_seqlens", n + 1, dev)
+    into = _index(torch, slots_out, "slots", n, dev)
+    start = into if slots_in is slots_out else _index(torch, slots_in, "slots_in", n, dev)
     p = Problem(n, total, cu, Hk, Hv, K, V, _token_stride(q, "q", lead, Hk, K),
-                _token_stride(k, "k", lead, Hk, K), _token_stride(v, "v", lead, Hv, V),
-                _index(torch, slots_in, "slots_in", n, dev), _index(torch, slots_out, "slots", n, dev),
+                _token_stride(k, "k", lead, Hk, K), _token_stride(v, "v", lead, Hv, V), start, into,
                 n if pool is None else pool, K ** -0.5 if scale is None else scale,
                 1 if normalize else 0, code)
     return p, n, (Hv, V, K)
@@ -148,16 +152,17 @@ class _On:
     __slots__ = ("torch", "device", "guard", "given", "handle")
 
     def __init__(self, torch, device, stream):
+        index = device.index
         if stream is None:
             # the handle of torch.cuda.current_stream(device), without the object around it: 1.8 us of a
             # single token's 14
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
         elif stream.device == device:
             self.handle = stream.cuda_stream
         else:
             raise ValueError(f"the stream must be one of {device}, not {stream.device}")
         self.torch, self.device, self.given = torch, device, stream
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -252,7 +257,7 @@ def gated_delta_forward(q, k, v, g, beta, s0=None, *, cu_seqlens=None, slots=Non
         if o is None:
             o = on.like(v)
         if s_out is None and want_state:
-            s_out = on.empty(states, torch.float32)
+            s_out = on.empty(states, torch.float32) if s0 is None else on.like(s0)
         ref = ctypes.byref(p)
         workspace, size = on.workspace(lib().gated_delta_forward_workspace(ref), workspace)
         _check(lib().gated_delta_forward(
@@ -308,7 +313,7 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
         u = on.like(v) if u is None else u
         s_ckpt = on.empty((chunks, *tail), q.dtype) if s_ckpt is None else s_ckpt
         if s_out is None and want_state:
-            s_out = on.empty((n, *tail), torch.float32)
+            s_out = on.empty((n, *tail), torch.float32) if s0 is None else on.like(s0)
         workspace, size = on.workspace(lib().gated_delta_forward_workspace(ref), workspace)
         _check(lib().gated_delta_forward_train(
             ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s0), _ptr(o), _ptr(s_out),
@@ -336,17 +341,16 @@ def gated_delta_backward(q, k, v, g, beta, d_o, s_ckpt, u, ds_T=None, *, cu_seql
     _dense(ds0, "ds0", (n, *tail), torch.float32, dev)
     if d_o is None or s_ckpt is None or u is None:
         raise ValueError("the backward needs d_o, s_ckpt and u")
-    shapes = (q.shape, k.shape, v.shape, g.shape, beta.shape)
     if grads is not None:
         if len(grads) != 5 or any(x is None for x in grads):
             raise ValueError("grads must hold the five gradient tensors (dq, dk, dv, dg, dbeta)")
-        for name, x, shape in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, shapes):
-            _dense(x, name, shape, dt, dev)
+        for name, x, like in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, (q, k, v, g, beta)):
+            _dense(x, name, like.shape, dt, dev)
     with _On(torch, dev, stream) as on:
         if grads is None:
-            grads = tuple(on.empty(shape, dt) for shape in shapes)
+            grads = tuple(on.like(x) for x in (q, k, v, g, beta))
         if ds0 is None and want_ds0:
-            ds0 = on.empty((n, *tail), torch.float32)
+            ds0 = on.empty((n, *tail), torch.float32) if ds_T is None else on.like(ds_T)
         workspace, size = on.workspace(lib().gated_delta_backward_workspace(ref), workspace)
         _check(lib().gated_delta_backward(
             ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(d_o), _ptr(s_ckpt), _ptr(u),
