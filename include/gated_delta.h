@@ -68,6 +68,11 @@ extern "C" {
 /* Tokens of a chunk: stored states are those at multiples of it. */
 #define GATED_DELTA_CHUNK 64
 
+/* Elements from one stored state (s_ckpt) to the next: V * K of the state and, in bf16,
+ * V * K / 4 for four more bits of each. */
+#define GATED_DELTA_CKPT_SIZE(V, K, dt) \
+    ((dt) == RWKV7_DT_BF16 ? (V) * (K) + (V) * (K) / 4 : (V) * (K))
+
 typedef struct {
     int n_seq;              /* sequences, >= 1                                          */
     int total;              /* rows (tokens) of q, k, v, g, beta, o; dense: n_seq * T    */
@@ -114,7 +119,9 @@ rwkv7_status gated_delta_decode(const gated_delta_problem *p, const void *q, con
 
 /*
  * Training forward: gated_delta_forward that also stores, for the backward,
- *   s_ckpt : [chunks, Hv, V, K] in dt, the state at the start of every chunk,
+ *   s_ckpt : [chunks, Hv, GATED_DELTA_CKPT_SIZE] in dt, the state at the start of
+ *            every chunk: [V, K] and, in bf16, four more bits of each element behind
+ *            it (for the gradient of g),
  *            chunks = gated_delta_chunks(p); sequence i's chunks begin at
  *            i * ceil(T / 64) (dense) or cu_seqlens[i] / 64 + i (packed)
  *   u      : [total, Hv, V] in dt, beta_t e_t of every token

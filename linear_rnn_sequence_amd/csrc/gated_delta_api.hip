@@ -34,7 +34,7 @@ struct Sizes {
     size_t q, k, v;          // extent of the strided inputs
     size_t qd, vd, gate;     // dense [total, Hk, K], [total, Hv, V], [total, Hv]
     size_t pool, states;     // float32 [pool, Hv, V, K], [n_seq, Hv, V, K]
-    size_t ckpt;             // dt [slots, Hv, V, K]
+    size_t ckpt;             // dt [slots, Hv, GATED_DELTA_CKPT_SIZE]
     size_t fwd, bwd;         // workspaces
     size_t fwd_seg;          // offset in the forward's
     size_t bwd_ds, bwd_dr;   // offsets in the backward's
@@ -101,7 +101,7 @@ rwkv7_status check_problem(const gated_delta_problem *in, Problem &p, Sizes &z) 
     if (!mul_ok(z.pool, (size_t)p.pool) || !mul_ok(z.states, (size_t)p.n_seq) ||
         !mul_ok(z.ckpt, (size_t)p.slots))
         return RWKV7_ERR_SHAPE;
-    z.ckpt = z.ckpt / 4 * esz;
+    z.ckpt = z.ckpt / 4 / (p.V * p.K) * GATED_DELTA_CKPT_SIZE(p.V, p.K, in->dt) * esz;
     z.fwd = forward_record_bytes(p.bf16);
     size_t rec = backward_record_bytes(p.bf16);
     if (!mul_ok(z.fwd, (size_t)p.Hv) || !mul_ok(z.fwd, (size_t)p.slots) ||

@@ -74,7 +74,40 @@ __device__ __forceinline__ void store_state(const State<K> &s, float *base, int 
     for (int m = 0; m < K / 16; ++m)
         *reinterpret_cast<f32x4 *>(base + lo * K + tile_row(m, 4 * g)) = s.t[m];
 }
-// the same rounded to E (the operand of the gradient kernel's products)
+// the same as a stored state (the gradient kernel's operand)
+template <class E, int K>
+__device__ __forceinline__ void store_kept(const State<K> &s, E *state, int V, int value0, int g,
+                                           int lo) {
+    constexpr int KS = K / 32;
+    E *row = state + (value0 + lo) * K;
+    unsigned word[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const f32x4 a = s.t[2 * ks], b = s.t[2 * ks + 1];
+        const Frag<E> f = to_frag<E>(a, b);
+        E *at = row + 32 * ks + 8 * g;
+        if constexpr (sizeof(E) == 2) {
+            *reinterpret_cast<u32x4 *>(at) = f.v;
+            word[ks] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                word[ks] |= (__float_as_uint(a[e]) >> 12 & 15u) << 4 * e;
+                word[ks] |= (__float_as_uint(b[e]) >> 12 & 15u) << (16 + 4 * e);
+            }
+        } else {
+            *reinterpret_cast<f32x4 *>(at) = f.v[0];
+            *reinterpret_cast<f32x4 *>(at + 4) = f.v[1];
+        }
+    }
+    if constexpr (sizeof(E) == 2) {
+        unsigned *at = reinterpret_cast<unsigned *>(state + V * K) + (value0 + lo) * (K / 8) + g * KS;
+        if constexpr (KS == 4)
+            *reinterpret_cast<u32x4 *>(at) = u32x4{word[0], word[1], word[2], word[3]};
+        else
+            *reinterpret_cast<u32x2 *>(at) = u32x2{word[0], word[1]};
+    }
+}
+// the same rounded to E (the operand of the combination's products)
 template <class E, int K>
 __device__ __forceinline__ void store_rounded(const State<K> &s, E *base, int g, int lo) {
 #pragma unroll
@@ -187,7 +220,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
     constexpr int KS = K / 32, kTile = L::kTile, kBuffer = L::kBuffer, kThreads = 64 * W;
     constexpr int kValues = 16 * W;
     // stores of an iteration behind its loads: the state (kTrain), u, and float's o
-    constexpr int kStores = (MODE == kTrain ? (K / 32 + 2) * (int)sizeof(E) / 2 : 0) +
+    constexpr int kStores = (MODE == kTrain ? (K / 32 + 2) * (int)sizeof(E) / 2 + 4 / (int)sizeof(E) - 1
+                                            : 0) +
                             (L::kShared || MODE == kSummary ? 0 : 4);
     extern __shared__ __align__(16) char lds[];
 
@@ -260,8 +294,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
     E *up = static_cast<E *>(p.mid) + token * row + hv * p.V + value0;
     const size_t rec_step = (size_t)p.Hv * Rec::kBytes;
     const char *rec = p.records + ((size_t)(sq.slot0 + c0) * p.Hv + hv) * Rec::kBytes;
-    E *states = static_cast<E *>(p.states) +
-                ((size_t)(sq.slot0 + c0) * p.Hv + hv) * state_size + (size_t)value0 * K;
+    const size_t kept = kept_size<E, K>(p.V);
+    E *states = static_cast<E *>(p.states) + ((size_t)(sq.slot0 + c0) * p.Hv + hv) * kept;
     using Values = Tile<E, L::kValueCols>;
 
     auto live_of = [&](int c) {
@@ -368,8 +402,6 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
         const float last = L::kRecord ? sc.last : last_next;
         const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)];
         if constexpr (!L::kShared) fetch_values(c + 1);
-        if (MODE == kTrain)
-            store_rounded<E>(S, states + (size_t)c * p.Hv * state_size, g, lo);
 
         // X = K S0^T [tokens, values]; O^T = S0 Q^T [values, tokens], so that a lane
         // ends up with four neighbouring values of a token
@@ -401,6 +433,8 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
             R[i] = tv.template column4<4>(tile_row(i, 4 * g), vcol, lane) + row_bcast4(kS, i) * X[i];
             if (MODE != kSummary) O[i] *= qs;
         }
+        if (MODE == kTrain)  // (157 us before these products, 138 us here)
+            store_kept<E>(S, states + (size_t)c * p.Hv * kept, p.V, value0, g, lo);
         // (keeps what is read from shared memory for the next products out of the
         // registers that these need)
         if (MODE != kSummary) __builtin_amdgcn_sched_barrier(0);
@@ -596,8 +630,8 @@ struct BackwardLds {
 // The same pipeline backwards: the rows of k and q and the record double-buffered; where
 // that does not fit (float, 128 keys) T^T and P^T are loaded again as soon as they have been
 // used.  It is bound by the length of the chain of products, one wave per SIMD: 4 x 2048
-// tokens, 32 heads of 128 x 128, take 151 us, 4.7 us a chunk, where the matrix cores are
-// busy 1 us; 177 us before the parts of split products were interleaved (mma_mixed).
+// tokens, 32 heads of 128 x 128, take 167 us, 5.2 us a chunk, where the matrix cores are
+// busy 1 us (26 us more before the parts of split products were interleaved, mma_mixed).
 template <class E, int K>
 __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p) {
     using Rec = BwdRecord<E>;
@@ -630,8 +664,8 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
     E *drp = static_cast<E *>(p.mid) + (long long)sq.begin * row + hv * p.V + value0;
     const size_t rec_step = (size_t)p.Hv * Rec::kBytes;
     const char *rec = p.records + ((size_t)sq.slot0 * p.Hv + hv) * Rec::kBytes;
-    E *states = static_cast<E *>(p.states) +
-                ((size_t)sq.slot0 * p.Hv + hv) * state_size + (size_t)value0 * K;
+    const size_t kept = kept_size<E, K>(p.V);
+    E *states = static_cast<E *>(p.states) + ((size_t)sq.slot0 * p.Hv + hv) * kept;
 
     auto live_of = [&](int c) {
         const int left = c >= 0 ? len - c * kChunk : 0;
@@ -697,7 +731,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
         // as many accesses behind these loads as the loop has
         const Buffer none(dvp, 0);
 #pragma unroll
-        for (int i = 0; i < (K / 32 + 4) * (int)sizeof(E) / 2; ++i)
+        for (int i = 0; i < (K / 32 + 4) * (int)sizeof(E) / 2 + 4 / (int)sizeof(E) - 1; ++i)
             none.store16(0, u32x4{0u, 0u, 0u, 0u});
     }
     for (int c = chunks - 1; c >= 0; --c) {
@@ -714,7 +748,6 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
         const float kS = sc.kS[own_token(lane)], kD = sc.kD[own_token(lane)],
                     beta = sc.beta[own_token(lane)];
         fetch_values(c - 1);
-        store_rounded<E>(D, states + (size_t)c * p.Hv * state_size, g, lo);
 
         // dU = diag(c_C / c) K D^T + P^T dO
         f32x4 X[4];
@@ -747,6 +780,7 @@ __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p
             for (int f = 0; f < 6; ++f)
                 X[kUpTile[f]] = mma_mixed(part, P[f], fo[kUpStep[f]], X[kUpTile[f]]);
         if constexpr (!L::kRecord) fetch_P(c - 1);
+        store_kept<E>(D, states + (size_t)c * p.Hv * kept, p.V, value0, g, lo);
         __builtin_amdgcn_sched_barrier(0);  // as in the forward
         // dR = T^T dU
         f32x4 R[4];

@@ -33,8 +33,8 @@
 // their way to registers while one is multiplied.
 //
 // What bounds it: 4 x 2048 tokens, 16 key heads of two value heads, 128 x 128 (2048
-// workgroups, one at a time on a CU) take 283 us, 76000 cycles a workgroup: 23000 of them
-// waiting for the first loads and the steps' (the bytes alone are 105 us), 14000 in the
+// workgroups, one at a time on a CU) take 304 us, about 80000 cycles a workgroup: 23000 of
+// them waiting for the first loads and the steps' (the bytes alone are 115 us), 14000 in the
 // steps' products, 17000 in the triangles and the products with k and q (half of it vector
 // instructions), 9000 in the sums for dg.  Shared memory (147 KB) and registers (128 of 16
 // waves) leave no room for a second workgroup, which would fill the waits, nor for loads
@@ -152,17 +152,31 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
     const bool upper = wave >= 8, with_states = wave < kStateThreads / 64;
     Stage<E, kVt, kChunk, 512> ga, gb;
     Stage<E, K, kVt, kStateThreads> gs, gd;
+    unsigned ws[gs.kPer], wd[gs.kPer];  // bf16: the pieces' further bits
     auto fetch = [&](int r, int v0) {
         const int hv = hk * rep + r;
         const int in = r < rep ? live : 0, rows = r < rep && with_states ? kVt : 0;
         const size_t at = (size_t)first * row + hv * p.V + v0;
-        const size_t st = ((size_t)slot * p.Hv + hv) * p.V * K + (size_t)v0 * K;
+        const size_t state = ((size_t)slot * p.Hv + hv) * kept_size<E, K>(p.V), st = state + (size_t)v0 * K;
         ga.load(static_cast<const E *>(upper ? p.dr : p.d_o) + at, row, in, tid & 511);
         gb.load(upper ? static_cast<const E *>(p.v) + (size_t)first * p.v_stride + hv * p.V + v0
                       : static_cast<const E *>(p.u) + at,
                 upper ? p.v_stride : row, in, tid & 511);
         gs.load(static_cast<const E *>(p.s_ckpt) + st, K, rows, tid);
         gd.load(static_cast<const E *>(p.ds) + st, K, rows, tid);
+        if constexpr (sizeof(E) == 2) {
+            const size_t at = state + (size_t)p.V * K + (size_t)v0 * (K / 4);
+            const Buffer bs(static_cast<const E *>(p.s_ckpt) + at, row_bytes<E>(rows, K / 4)),
+                bd(static_cast<const E *>(p.ds) + at, row_bytes<E>(rows, K / 4));
+#pragma unroll
+            for (int i = 0; i < gs.kPer; ++i) {
+                const int piece = tid + i * kStateThreads;
+                const int row = piece / (K / 8), col = piece % (K / 8);  // in pieces
+                const unsigned word = (unsigned)(row * (K / 8) + (col & 3) * (K / 32) + (col >> 2));
+                ws[i] = __float_as_uint(bs.load_float(word * 4u));
+                wd[i] = __float_as_uint(bd.load_float(word * 4u));
+            }
+        }
     };
     {
         constexpr int kRowThreads = L::kRows / 16 < kThreads ? L::kRows / 16 : kThreads;
@@ -232,13 +246,37 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
                 gd.store(td, tid);
             }
             if (upper) drv = dot_piece<E>(ga.x[0], gb.x[0], drv);  // eight lanes per token
+            unsigned ms[gs.kPer], md[gs.kPer];
 #pragma unroll
-            for (int i = 0; i < gs.kPer; ++i) ds_sum = dot_piece<E>(gs.x[i], gd.x[i], ds_sum);
+            for (int i = 0; i < gs.kPer; ++i) {
+                if constexpr (sizeof(E) == 2) {
+                    ms[i] = ws[i];
+                    md[i] = wd[i];
+                } else {
+                    ds_sum = dot_piece<E>(gs.x[i], gd.x[i], ds_sum);
+                }
+            }
             if (j + 1 < steps)
                 fetch(r, (j + 1) * kVt);
             else
                 fetch(r + 1, 0);
             __syncthreads();
+            if constexpr (sizeof(E) == 2) {  // S0 D: its own pieces again, the loads are under way
+                if (with_states)
+#pragma unroll
+                    for (int i = 0; i < gs.kPer; ++i) {
+                        const int piece = tid + i * kStateThreads;
+                        const int at = ts.offset(piece / (K / 8), piece % (K / 8) * 8);
+                        const u32x4 s = *reinterpret_cast<const u32x4 *>(ts.p + at),
+                                    d = *reinterpret_cast<const u32x4 *>(td.p + at);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const unsigned a = s[x >> 1], b = d[x >> 1];
+                            ds_sum += kept_float(x & 1 ? a & 0xffff0000u : a << 16, ms[i], x) *
+                                      kept_float(x & 1 ? b & 0xffff0000u : b << 16, md[i], x);
+                        }
+                    }
+            }
             const Tile<E, kVt> ta = part < 2 ? tu : part == 2 ? to : tr,
                                tb = part == 0 ? to : part == 1 ? tr : tu;
 #pragma unroll

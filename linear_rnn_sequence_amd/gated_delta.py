@@ -94,6 +94,24 @@ def _dense(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _ckpt_size(torch, V, K, dtype):
+    """Elements from state to state of the stored ones (GATED_DELTA_CKPT_SIZE)."""
+    return V * K + V * K // 4 if dtype == torch.bfloat16 else V * K
+
+
+def _check_ckpt(torch, t, chunks, tail, dtype, device):
+    """The states that the training forward stores: [chunks,Hv,V,K], GATED_DELTA_CKPT_SIZE apart with the
+    further bits behind each, the last one as well."""
+    Hv, V, K = tail
+    size = _ckpt_size(torch, V, K, dtype)
+    if t.shape != (chunks, *tail) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"s_ckpt: {tuple(t.shape)} {t.dtype} on {t.device}, expected {(chunks, *tail)} {dtype} "
+                         f"on {device}")
+    if chunks and (t.stride() != (Hv * size, size, K, 1) or t.untyped_storage().nbytes() <
+                   (t.storage_offset() + chunks * Hv * size) * t.element_size()):
+        raise ValueError("s_ckpt must be the tensor that gated_delta_forward_train returned")
+
+
 def _index(torch, t, name, n, device):
     if t is None:
         return None
@@ -295,7 +313,8 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
                               normalize=False, o=None, s_out=None, want_state=True, s_ckpt=None,
                               u=None, workspace=None, stream=None):
     """gated_delta_forward_train.  Returns (o, s_out, s_ckpt, u); s_ckpt [chunks,Hv,V,K] and u (like
-    v), in the inputs' dtype, are what :func:`gated_delta_backward` needs besides the inputs."""
+    v), in the inputs' dtype, are what :func:`gated_delta_backward` needs besides the inputs (bf16
+    states have further bits behind each, which a copy of the tensor would lose: it is refused)."""
     import torch
 
     _check_ranks(q, k, v, g, beta)
@@ -306,12 +325,16 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
     _dense(s0, "s0", (n, *tail), torch.float32, dev)
     _dense(s_out, "s_out", (n, *tail), torch.float32, dev)
     _dense(o, "o", v.shape, q.dtype, dev)
-    _dense(s_ckpt, "s_ckpt", (chunks, *tail), q.dtype, dev)
+    if s_ckpt is not None:
+        _check_ckpt(torch, s_ckpt, chunks, tail, q.dtype, dev)
     _dense(u, "u", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
         o = on.like(v) if o is None else o
         u = on.like(v) if u is None else u
-        s_ckpt = on.empty((chunks, *tail), q.dtype) if s_ckpt is None else s_ckpt
+        if s_ckpt is None:
+            Hv, V, K = tail
+            size = _ckpt_size(torch, V, K, q.dtype)
+            s_ckpt = on.empty((chunks * Hv * size,), q.dtype).as_strided((chunks, *tail), (Hv * size, size, K, 1))
         if s_out is None and want_state:
             s_out = on.empty((n, *tail), torch.float32) if s0 is None else on.like(s0)
         workspace, size = on.workspace(lib().gated_delta_forward_workspace(ref), workspace)
@@ -335,7 +358,8 @@ def gated_delta_backward(q, k, v, g, beta, d_o, s_ckpt, u, ds_T=None, *, cu_seql
     dev, dt = q.device, q.dtype
     ref = ctypes.byref(p)
     _dense(d_o, "d_o", v.shape, dt, dev)
-    _dense(s_ckpt, "s_ckpt", (lib().gated_delta_chunks(ref), *tail), dt, dev)
+    if s_ckpt is not None:
+        _check_ckpt(torch, s_ckpt, lib().gated_delta_chunks(ref), tail, dt, dev)
     _dense(u, "u", v.shape, dt, dev)
     _dense(ds_T, "ds_T", (n, *tail), torch.float32, dev)
     _dense(ds0, "ds0", (n, *tail), torch.float32, dev)

@@ -638,3 +638,36 @@ def test_offsets_behind_32_bits(rnn):
     close_state(grads[5][1], f64(want[5][0]), "bf16", "ds0")
     plain, _ = rnn.gated_delta_forward(*x, cu_seqlens=cu, normalize=True, want_state=False)
     assert torch.equal(plain[:, T - 200:], o[:, T - 200:])
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128), (128, 64)])
+@pytest.mark.parametrize("T", [1, 64])
+def test_decay_gradient_keeps_the_product_of_the_states(rnn, K, V, T):
+    """With nothing written (beta = 0) and nothing read (d_o = 0), dg of every token is the whole decay
+    times <S0, dS_T>: a sum of V K products of either sign, often small next to them.  The stored states
+    keep 12 bits of significand for it, off by at most 2^-12: a product by 2^-11, and V K of them,
+    uniformly and independently, by 2^-11 / sqrt(6) of their root sum of squares; six times that is 2^-9.7.
+    (Factors of 8 bits would be off by 2^-8.3 in the mean.)"""
+    B = 128
+    x = inputs(B * T, 1, 1, K, V, "bf16", 111, B=B, slow=True)
+    x["beta"].zero_()
+    x["g"] *= 1 / T
+    s0, ds = states(B, 1, V, K, 12), states(B, 1, V, K, 13)
+    d_o = torch.zeros_like(x["v"])
+    o, s, ck, u = rnn.gated_delta_forward_train(*x.values(), s0=s0, normalize=True)
+    dg = f64(rnn.gated_delta_backward(*x.values(), d_o, ck, u, ds_T=ds, normalize=True)[3])[..., 0]
+    c = np.exp(f64(x["g"])[..., 0].sum(1))
+    terms = (f64(s0) * f64(ds)).reshape(B, -1)
+    want, size = c * terms.sum(1), c * np.sqrt((terms ** 2).sum(1))
+    off = np.abs(dg - want[:, None])
+    assert (off <= 2.0 ** -8 * np.abs(want[:, None]) + 2.0 ** -9.7 * size[:, None]).all(), (off / size[:, None]).max()
+
+
+def test_a_copy_of_the_stored_states_is_refused(rnn):
+    x = inputs(100, 1, 1, 64, 64, "bf16", 112)
+    o, s, ck, u = rnn.gated_delta_forward_train(*x.values())
+    d_o = torch.ones_like(o)
+    rnn.gated_delta_backward(*x.values(), d_o, ck, u)
+    for bad in (ck.contiguous(), ck.clone(), ck[:1], ck.float()):
+        with pytest.raises(ValueError):
+            rnn.gated_delta_backward(*x.values(), d_o, bad, u)
