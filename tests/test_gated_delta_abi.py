@@ -219,3 +219,22 @@ def test_tokens_in_each_others_place_are_refused():
             G._token_stride(bad, "q", (5,), 7, 64)
     assert G._token_stride(one[..., :3, :], "q", (1, 1), 3, 64) in (0, 3 * 64)
     assert G._token_stride(one[:0], "q", (0, 1), 7, 64) in (0, 7 * 64)
+
+
+def test_stored_states_need_the_bits_behind_them():
+    """bf16 states lie 5/4 V K apart; a copy without what lies behind them, and a view whose memory ends with the
+    last state, are refused on the host."""
+    cpu, tail, chunks = torch.device("cpu"), (2, 64, 128), 3
+    size = G._ckpt_size(torch, 64, 128, torch.bfloat16)
+    assert size == 64 * 128 * 5 // 4 and G._ckpt_size(torch, 64, 128, torch.float32) == 64 * 128
+    strides = (2 * size, size, 128, 1)
+    whole = torch.zeros(chunks * 2 * size, dtype=torch.bfloat16)
+    good = whole.as_strided((chunks, *tail), strides)
+    G._check_ckpt(torch, good, chunks, tail, torch.bfloat16, cpu)
+    short = torch.zeros(chunks * 2 * size - 64 * 32, dtype=torch.bfloat16).as_strided((chunks, *tail), strides)
+    for bad in (good.contiguous(), good[1:], short, good.float()):
+        with pytest.raises(ValueError):
+            G._check_ckpt(torch, bad, chunks, tail, torch.bfloat16, cpu)
+    with pytest.raises(ValueError):  # the same rows, further on in the memory
+        G._check_ckpt(torch, whole.as_strided((2, *tail), strides, 2 * size + 128), 2, tail, torch.bfloat16, cpu)
+    G._check_ckpt(torch, torch.zeros(chunks, *tail), chunks, tail, torch.float32, cpu)

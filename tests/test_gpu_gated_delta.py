@@ -671,3 +671,31 @@ def test_a_copy_of_the_stored_states_is_refused(rnn):
     for bad in (ck.contiguous(), ck.clone(), ck[:1], ck.float()):
         with pytest.raises(ValueError):
             rnn.gated_delta_backward(*x.values(), d_o, bad, u)
+
+
+@pytest.mark.parametrize("layout", [("bf16", 64, 128, 1, 1), ("bf16", 128, 128, 1, 2), ("f32", 64, 64, 1, 1)], ids=str)
+def test_gradients_of_a_sequence_in_segments(rnn, layout):
+    """A training step whose forward is done in segments, next to a short and an empty sequence."""
+    dtype, K, V, Hk, Hv = layout
+    lens = [3300, 0, 70]
+    cu = np.cumsum([0] + lens)
+    x = inputs(int(cu[-1]), Hk, Hv, K, V, dtype, 120, slow=True)
+    s0, ds = states(3, Hv, V, K, 1), states(3, Hv, V, K, 2)
+    d_o = torch.from_numpy(np.random.default_rng(9).normal(size=(1, int(cu[-1]), Hv, V))).to(DT[dtype]).cuda()
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    need = rnn.gated_delta_forward_workspace_bytes
+    assert need(int(cu[-1]), Hk, Hv, K, V, sequences=3, packed=True, dtype=dtype) > \
+        need(64, 1, 1, K, V, dtype=dtype) * Hv * (int(cu[-1]) // 64 + 3)
+    o, s, ck, u = rnn.gated_delta_forward_train(*x.values(), s0=s0, cu_seqlens=cut, normalize=True)
+    grads = rnn.gated_delta_backward(*x.values(), d_o, ck, u, ds_T=ds, cu_seqlens=cut, normalize=True)
+    for i in range(3):
+        a, b = cu[i], cu[i + 1]
+        want, S, trace = gd.forward(*rows(x, 0, a, b), f64(s0[i]), normalize=True)
+        ref = gd.backward(*rows(x, 0, a, b), f64(d_o[0, a:b]), f64(ds[i]), f64(s0[i]), normalize=True)
+        close(o[0, a:b], want, dtype, "o")
+        close_state(s[i], S, dtype)
+        for c in range((lens[i] + 63) // 64):
+            close(ck[a // 64 + i + c], trace[64 * c], dtype, f"state {c} of sequence {i}")
+        for name, got, w in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, ref):
+            close(got[0, a:b], w, dtype, f"{name} of sequence {i}")
+        close_state(grads[5][i], ref[5], dtype, "ds0")
