@@ -62,7 +62,6 @@ struct Frag;
 template <>
 struct Frag<bf16_t> {
     u32x4 v;
-    static __device__ __forceinline__ Frag zero() { return Frag{u32x4{0u, 0u, 0u, 0u}}; }
     __device__ __forceinline__ float at(int j) const {
         const unsigned u = v[j >> 1];
         return __uint_as_float((j & 1) ? (u & 0xffff0000u) : (u << 16));
@@ -71,9 +70,6 @@ struct Frag<bf16_t> {
 template <>
 struct Frag<float> {
     f32x4 v[2];
-    static __device__ __forceinline__ Frag zero() {
-        return Frag{{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}};
-    }
     __device__ __forceinline__ float at(int j) const { return v[j >> 2][j & 3]; }
 };
 
@@ -100,30 +96,11 @@ __device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Frag<float> &b,
                                                  0);
     return c;
 }
-// exact A, float B (and the other way round)
-__device__ __forceinline__ f32x4 mma(const Frag<bf16_t> &a, const Split<bf16_t> &b, f32x4 c) {
-    return mma(a, b.hi, mma(a, b.lo, c));
-}
-__device__ __forceinline__ f32x4 mma(const Split<bf16_t> &a, const Frag<bf16_t> &b, f32x4 c) {
-    return mma(a.hi, b, mma(a.lo, b, c));
-}
-// both float: the product of the two lo parts (2^-18 of the whole) is left out
-__device__ __forceinline__ f32x4 mma(const Split<bf16_t> &a, const Split<bf16_t> &b, f32x4 c) {
-    return mma(a.hi, b.hi, mma(a.hi, b.lo, mma(a.lo, b.hi, c)));
-}
-__device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Split<float> &b, f32x4 c) {
-    return mma(a, b.hi, c);
-}
-__device__ __forceinline__ f32x4 mma(const Split<float> &a, const Frag<float> &b, f32x4 c) {
-    return mma(a.hi, b, c);
-}
-__device__ __forceinline__ f32x4 mma(const Split<float> &a, const Split<float> &b, f32x4 c) {
-    return mma(a.hi, b.hi, c);
-}
-
-// The parts of those products one at a time, smallest first: a kernel that has
-// several results to add to does one part for all of them before the next, so that
-// no instruction waits for the one before it.  Float operands have one part.
+// Products with a float operand (mixed: the other one is exact) or two (split: the product of
+// the two lo parts, 2^-18 of the whole, is left out) in their parts, one at a time,
+// smallest first: a kernel that has several results to add to does one part for all of
+// them before the next, so that no instruction waits for the one before it.  Float
+// operands have one part.
 template <class E>
 constexpr int kPartsMixed = sizeof(E) == 2 ? 2 : 1;  // one operand split
 template <class E>
@@ -295,9 +272,6 @@ struct Tile {
             return f32x4{p[offset(row0, col)], p[offset(row0 + 1, col)], p[offset(row0 + 2, col)],
                          p[offset(row0 + 3, col)]};
         }
-    }
-    __device__ __forceinline__ float at(int row, int col) const {
-        return to_float(p[offset(row, col)]);
     }
 };
 template <class E, int C>
