@@ -572,24 +572,26 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
                     ((size_t)sq.slot0 * p.Hv + at.hv) * (kPlanes * K * K);
     const Tile<E, K> tm[2] = {Tile<E, K>{reinterpret_cast<E *>(lds)},
                               Tile<E, K>{reinterpret_cast<E *>(lds + tile_bytes<E, K>(K))}};
-    Stage<E, K, K, kThreads> gm[kPlanes];
-    State<K> S, next;
+    // the transitions and states of the next steps, on their way (with 128 keys there are
+    // registers for one)
+    constexpr int kAhead = K == 64 ? 2 : 1;
+    Stage<E, K, K, kThreads> gm[kAhead][kPlanes];
+    State<K> S, next[kAhead];
     load_state(S, state, g, lo);
-    auto fetch = [&](int j) {
+    auto fetch = [&](int set, int j) {
 #pragma unroll
         for (int x = 0; x < kPlanes; ++x)
-            gm[x].load(step + (size_t)j * p.Hv * (kPlanes * K * K) + x * K * K, K,
-                       j < segments - 1 ? K : 0, tid);
-        if (j < segments - 1) load_state(next, state + (size_t)j * p.Hv * state_size, g, lo);
+            gm[set][x].load(step + (size_t)j * p.Hv * (kPlanes * K * K) + x * K * K, K,
+                            j < segments - 1 ? K : 0, tid);
+        if (j < segments - 1) load_state(next[set], state + (size_t)j * p.Hv * state_size, g, lo);
     };
-    fetch(1);
-    for (int j = 1; j < segments - 1; ++j) {
+    auto one = [&](int set, int j) {
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < kPlanes; ++x) gm[x].store(tm[x], tid);
+        for (int x = 0; x < kPlanes; ++x) gm[set][x].store(tm[x], tid);
         __syncthreads();
-        State<K> R = next;
-        fetch(j + 1);
+        State<K> R = next[set];
+        fetch(set, j + kAhead);
 #pragma unroll
         for (int ks = 0; ks < K / 32; ++ks) {
             const Split<E> b = to_split<E>(S.t[2 * ks], S.t[2 * ks + 1]);
@@ -611,6 +613,12 @@ __global__ __launch_bounds__(kThreads, 1) void combine_kernel(ChainArgs p) {
         }
         S = R;
         store_state(S, state + (size_t)j * p.Hv * state_size, g, lo);
+    };
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) fetch(x, 1 + x);
+    for (int j = 1; j < segments - 1; j += kAhead) {
+        one(0, j);
+        if (kAhead == 2 && j + 1 < segments - 1) one(kAhead - 1, j + 1);
     }
 }
 
