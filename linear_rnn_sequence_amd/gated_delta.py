@@ -2,7 +2,9 @@
 
 Argument marshalling only, as in :mod:`.wkv`: the kernels of librwkv7_wkv.so do the work,
 torch provides device memory and the stream.  Calls run on the tensors' device and, unless a
-stream is given, on that device's current stream.
+stream is given, on that device's current stream.  A given stream does not wait for the current
+one, nor the other way round: the caller orders it behind what makes the inputs, and what reads
+the results behind it.  The memory on both sides is safe to free at any time.
 
 Shapes: q, k [B,T,Hk,K], v [B,T,Hv,V], g and beta [B,T,Hv] (g: log decay), one dtype
 (torch.bfloat16 or torch.float32); states float32 [B,Hv,V,K].  A packed batch of n sequences has
@@ -165,22 +167,26 @@ def _check_ranks(q, k, v, g, beta):
 
 
 class _On:
-    """The tensors' device as the current one, and the stream a call goes to."""
+    """The tensors' device as the current one, and the stream a call goes to.  With a given stream, the
+    call's memory belongs to it too: memory of the current stream may still be in use by what that
+    stream has queued (its last owner was freed on the host), which the given one does not wait for."""
 
-    __slots__ = ("torch", "device", "guard", "given", "handle")
+    __slots__ = ("torch", "device", "guard", "given", "caller", "handle")
 
     def __init__(self, torch, device, stream):
         index = device.index
+        self.torch, self.device, self.given = torch, device, stream
         if stream is None:
             # the handle of torch.cuda.current_stream(device), without the object around it: 1.8 us of a
             # single token's 14
             self.handle = torch._C._cuda_getCurrentRawStream(index)
+            self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(device)
         elif stream.device == device:
             self.handle = stream.cuda_stream
+            self.caller = torch.cuda.current_stream(device)
+            self.guard = torch.cuda.stream(stream)  # its device too
         else:
             raise ValueError(f"the stream must be one of {device}, not {stream.device}")
-        self.torch, self.device, self.given = torch, device, stream
-        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -192,11 +198,20 @@ class _On:
             self.guard.__exit__(*exc)
         return False
 
+    def uses(self, *tensors):
+        """The caller's tensors: freed after the call, their memory is not handed out again before a given
+        stream's work is done."""
+        if self.given is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.given)
+
     def empty(self, shape, dtype):
-        """Memory for the call: it is not handed out again before a given stream's work is done."""
+        """Memory for the caller: freed, it is not handed out again before the work that the caller's
+        stream has queued by then is done either."""
         t = self.torch.empty(shape, dtype=dtype, device=self.device)
         if self.given is not None:
-            t.record_stream(self.given)
+            t.record_stream(self.caller)
         return t
 
     def like(self, x):
@@ -206,10 +221,11 @@ class _On:
         return self.torch.empty_like(x)
 
     def workspace(self, need, given):
-        if given is None:
-            return self.empty((need,), self.torch.uint8) if need else None, need
+        if given is None:  # the call's alone
+            return self.torch.empty((need,), dtype=self.torch.uint8, device=self.device) if need else None, need
         if not given.is_contiguous() or given.device != self.device:
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
+        self.uses(given)
         return given, given.numel() * given.element_size()
 
 
@@ -272,6 +288,7 @@ def gated_delta_forward(q, k, v, g, beta, s0=None, *, cu_seqlens=None, slots=Non
     _dense(s_out, "s_out", states, torch.float32, dev)
     _dense(o, "o", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
+        on.uses(q, k, v, g, beta, s0, o, s_out, cu_seqlens, slots, slots_in)
         if o is None:
             o = on.like(v)
         if s_out is None and want_state:
@@ -301,6 +318,7 @@ def gated_delta_decode(q, k, v, g, beta, state, *, slots=None, scale=None, norma
     _dense(state, "state", (p.pool, *tail), torch.float32, dev)
     _dense(o, "o", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
+        on.uses(q, k, v, g, beta, state, o, slots)
         if o is None:
             o = on.like(v)
         _check(lib().gated_delta_decode(
@@ -329,6 +347,7 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
         _check_ckpt(torch, s_ckpt, chunks, tail, q.dtype, dev)
     _dense(u, "u", v.shape, q.dtype, dev)
     with _On(torch, dev, stream) as on:
+        on.uses(q, k, v, g, beta, s0, o, s_out, s_ckpt, u, cu_seqlens)
         o = on.like(v) if o is None else o
         u = on.like(v) if u is None else u
         if s_ckpt is None:
@@ -371,6 +390,7 @@ def gated_delta_backward(q, k, v, g, beta, d_o, s_ckpt, u, ds_T=None, *, cu_seql
         for name, x, like in zip(("dq", "dk", "dv", "dg", "dbeta"), grads, (q, k, v, g, beta)):
             _dense(x, name, like.shape, dt, dev)
     with _On(torch, dev, stream) as on:
+        on.uses(q, k, v, g, beta, d_o, s_ckpt, u, ds_T, ds0, cu_seqlens, *(grads or ()))
         if grads is None:
             grads = tuple(on.like(x) for x in (q, k, v, g, beta))
         if ds0 is None and want_ds0:
@@ -408,6 +428,7 @@ def state_move(pool, src, dst, *, slot_dim=0, stream=None):
     _index(torch, dst, "dst", n, dev)
     step = pool.stride(0) * pool.element_size() if slot_dim and layers > 1 else 0
     with _On(torch, dev, stream) as on:
+        on.uses(pool, src, dst)
         _check(lib().state_move(_ptr(pool), layers, step, slots, size, _ptr(src), _ptr(dst), n, on.handle),
                "state_move")
     return pool
