@@ -114,6 +114,34 @@ def _stream(torch, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(torch, stream, shape, dtype, device, returned=True):
+    """Memory for a call on `stream` (None: the current one).  It belongs to that stream: memory of
+    the current one may still be in use by what that has queued (its last owner was freed on the
+    host), which a given stream does not wait for.  What is returned to the caller may be freed
+    while the caller's stream still reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(caller)
+    return t
+
+
+def _used_on(stream, *tensors):
+    """The caller's tensors of a call on a given stream: freed after the call, their memory is not
+    handed out again before that stream's work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _epilogue_tensors(epilogue):
+    return () if epilogue is None else tuple(epilogue.get(n) for n in ("ln_w", "ln_b", "r_k"))
+
+
 def _epilogue(epilogue):
     if epilogue is None:
         return None, ()
@@ -222,13 +250,14 @@ def forward(r, w, k, v, kappa, a, s0=None, *, algo="auto", epilogue=None, y=None
     _check_tensor(torch, s_out, "s_out", (B, H, N, N), f32, dev)
     _check_epilogue(torch, epilogue, H, N, dev)
     _check_workspace(torch, workspace, dev)
+    _used_on(stream, r, w, k, v, kappa, a, s0, y, s_out, workspace, *_epilogue_tensors(epilogue))
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, dev)
     if s_out is None and want_state:
-        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        s_out = _empty(torch, stream, (B, H, N, N), f32, dev)
     need = lib().rwkv7_wkv_forward_workspace(B, T, H, N, dt, ALGOS[algo])
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _empty(torch, stream, (need,), torch.uint8, dev, returned=False)
     epi_ptr, keep = _epilogue(epilogue)
     code = lib().rwkv7_wkv_forward(
         _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a), _ptr(s0), _ptr(y),
@@ -258,6 +287,7 @@ def forward_noalloc(r, w, k, v, kappa, a, s0=None, *, y, s_out=None, algo="auto"
     _check_tensor(torch, y, "y", r.shape, r.dtype, dev)
     _check_tensor(torch, s_out, "s_out", (B, H, N, N), f32, dev)
     _check_epilogue(torch, epilogue, H, N, dev)
+    _used_on(stream, r, w, k, v, kappa, a, s0, y, s_out, *_epilogue_tensors(epilogue))
     epi_ptr, keep = _epilogue(epilogue)
     code = lib().rwkv7_wkv_forward_noalloc(
         _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a), _ptr(s0), _ptr(y),
@@ -289,13 +319,14 @@ def forward_fused(r, w, k, v, a, k_k, k_a, g=None, s0=None, *, algo="auto", epil
     _check_tensor(torch, s_out, "s_out", (B, H, N, N), f32, dev)
     _check_epilogue(torch, epilogue, H, N, dev)
     _check_workspace(torch, workspace, dev)
+    _used_on(stream, r, w, k, v, a, k_k, k_a, g, s0, y, s_out, workspace, *_epilogue_tensors(epilogue))
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, dev)
     if s_out is None and want_state:
-        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        s_out = _empty(torch, stream, (B, H, N, N), f32, dev)
     need = lib().rwkv7_wkv_forward_workspace(B, T, H, N, dt, ALGOS[algo])
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _empty(torch, stream, (need,), torch.uint8, dev, returned=False)
     pro = Prologue(k_k=k_k.data_ptr(), k_a=k_a.data_ptr(),
                    g=None if g is None else g.data_ptr())
     epi_ptr, keep = _epilogue(epilogue)
@@ -325,13 +356,14 @@ def forward_bidir(r, w, k, v, kappa, a, s0=None, *, algo="auto", epilogue=None, 
     _check_tensor(torch, s_out, "s_out", (2, B, H, N, N), f32, dev)
     _check_epilogue(torch, epilogue, H, N, dev)
     _check_workspace(torch, workspace, dev)
+    _used_on(stream, r, w, k, v, kappa, a, s0, y, s_out, workspace, *_epilogue_tensors(epilogue))
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, dev)
     if s_out is None and want_state:
-        s_out = torch.empty((2, B, H, N, N), dtype=torch.float32, device=r.device)
+        s_out = _empty(torch, stream, (2, B, H, N, N), f32, dev)
     need = lib().rwkv7_wkv_forward_bidir_workspace(B, T, H, N, dt, ALGOS[algo])
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _empty(torch, stream, (need,), torch.uint8, dev, returned=False)
     epi_ptr, keep = _epilogue(epilogue)
     code = lib().rwkv7_wkv_forward_bidir(
         _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a), _ptr(s0), _ptr(y),
@@ -367,15 +399,16 @@ def forward_train(r, w, k, v, kappa, a, s0=None, *, algo="auto", y=None, s_out=N
     _check_tensor(torch, s_out, "s_out", (B, H, N, N), f32, dev)
     _check_tensor(torch, s_ckpt, "s_ckpt", (B, H, nck, N, N), f32, dev)
     _check_workspace(torch, workspace, dev)
+    _used_on(stream, r, w, k, v, kappa, a, s0, y, s_out, s_ckpt, workspace)
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, dev)
     if s_out is None and want_state:
-        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        s_out = _empty(torch, stream, (B, H, N, N), f32, dev)
     if s_ckpt is None:
-        s_ckpt = torch.empty((B, H, nck, N, N), dtype=torch.float32, device=r.device)
+        s_ckpt = _empty(torch, stream, (B, H, nck, N, N), f32, dev)
     need = lib().rwkv7_wkv_forward_workspace(B, T, H, N, dt, ALGOS[algo])
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _empty(torch, stream, (need,), torch.uint8, dev, returned=False)
     code = lib().rwkv7_wkv_forward_train(
         _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a), _ptr(s0), _ptr(y),
         _ptr(s_out), _ptr(s_ckpt), B, T, H, N, dt, ALGOS[algo], _ptr(workspace),
@@ -420,13 +453,15 @@ def backward(r, w, k, v, kappa, a, dy, s_ckpt, ds_T=None, *, grads=None, ds0=Non
             _check_tensor(torch, gt, name, r.shape, w.dtype if i == 1 else r.dtype, dev)
             if gt is None:
                 raise ValueError(f"{name} is required")
+    _used_on(stream, r, w, k, v, kappa, a, dy, s_ckpt, ds_T, ds0, workspace, *(grads or ()))
     if grads is None:
-        grads = tuple(torch.empty_like(w if i == 1 else r) for i in range(6))
+        grads = tuple(_empty(torch, stream, r.shape, w.dtype if i == 1 else r.dtype, dev)
+                      for i in range(6))
     if ds0 is None and want_ds0:
-        ds0 = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        ds0 = _empty(torch, stream, (B, H, N, N), f32, dev)
     need = int(lib().rwkv7_wkv_backward_workspace(B, T, H, N, dt, ALGOS[algo]))
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _empty(torch, stream, (need,), torch.uint8, dev, returned=False)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     code = lib().rwkv7_wkv_backward(
         _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a), _ptr(dy), _ptr(s_ckpt),
@@ -449,8 +484,9 @@ def decode(r, w, k, v, kappa, a, state, *, epilogue=None, y=None, stream=None):
         raise ValueError("decode needs the state")
     _check_tensor(torch, y, "y", r.shape, r.dtype, r.device)
     _check_epilogue(torch, epilogue, H, N, r.device)
+    _used_on(stream, r, w, k, v, kappa, a, state, y, *_epilogue_tensors(epilogue))
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, r.device)
     epi_ptr, keep = _epilogue(epilogue)
     code = lib().rwkv7_wkv_decode(_ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(kappa), _ptr(a),
                                   _ptr(state), _ptr(y), B, H, N, dt, epi_ptr,
@@ -481,8 +517,9 @@ def decode_fused(r, w, k, v, a, k_k, k_a, state, *, g=None, epilogue=None, y=Non
         raise ValueError("decode needs the state")
     _check_tensor(torch, y, "y", r.shape, r.dtype, r.device)
     _check_epilogue(torch, epilogue, H, N, r.device)
+    _used_on(stream, r, w, k, v, a, k_k, k_a, g, state, y, *_epilogue_tensors(epilogue))
     if y is None:
-        y = torch.empty_like(r)
+        y = _empty(torch, stream, r.shape, r.dtype, r.device)
     pro = Prologue(k_k=k_k.data_ptr(), k_a=k_a.data_ptr(),
                    g=None if g is None else g.data_ptr())
     epi_ptr, keep = _epilogue(epilogue)
@@ -536,6 +573,7 @@ def stream_copy(src, dst, *, stream=None):
     nbytes = src.numel() * src.element_size()
     if dst.numel() * dst.element_size() != nbytes:
         raise ValueError("stream_copy needs tensors of equal byte size")
+    _used_on(stream, src, dst)
     code = lib().rwkv7_stream_copy(_ptr(src), _ptr(dst), nbytes, _stream(torch, stream))
     if code != 0:
         raise Rwkv7Error(code, "rwkv7_stream_copy")

@@ -116,3 +116,42 @@ def test_gated_delta_inputs_may_be_freed_at_once(rnn):
         torch.empty(shape, dtype=torch.bfloat16, device="cuda").fill_(7)
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(s, want[1])
+
+
+def wkv_calls(rnn):
+    B, T, H, N = 2, 400, 3, 64
+    g = torch.Generator("cuda").manual_seed(3)
+    new = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    kappa = torch.nn.functional.normalize(new(B, T, H, N), dim=-1)
+    x = [t.bfloat16() for t in (new(B, T, H, N), new(B, T, H, N).sigmoid() * 0.5 + 0.5, new(B, T, H, N), new(B, T, H, N),
+                                kappa, new(B, T, H, N).sigmoid())]
+    r, w, k, v, kappa, a = x
+    y, s, ck = rnn.forward_train(*x)
+    dy = torch.randn_like(y)
+    key = [torch.ones(H * N, device="cuda"), torch.ones(H * N, device="cuda")]
+    states = torch.randn(1, B, H, N, N, device="cuda").expand(4, -1, -1, -1, -1).contiguous()
+    left = list(states)
+    one = [t[:, 0].contiguous() for t in x]
+    fwd, bwd = rnn.forward_workspace_bytes(B, T, H), rnn.backward_workspace_bytes(B, T, H)
+    return {
+        "forward": (lambda **o: rnn.forward(*x, **o), fwd),
+        "bidir": (lambda **o: rnn.forward_bidir(*x, **o), rnn.forward_bidir_workspace_bytes(B, T, H)),
+        "fused": (lambda **o: rnn.forward_fused(r, w, k, v, a, *key, **o), fwd),
+        "train": (lambda **o: rnn.forward_train(*x, **o), fwd),
+        "backward": (lambda **o: rnn.backward(*x, dy, ck, **o), bwd),
+        "decode": (lambda **o: rnn.decode(*one, left.pop(), **o), 0),
+    }
+
+
+WKV = ["forward", "bidir", "fused", "train", "backward", "decode"]
+
+
+@pytest.mark.parametrize("name", WKV)
+def test_wkv_leaves_busy_memory_alone(rnn, name):
+    call, work = wkv_calls(rnn)[name]
+    check_busy_memory(call, work)
+
+
+@pytest.mark.parametrize("name", WKV)
+def test_wkv_results_may_be_freed_at_any_time(rnn, name):
+    check_results_freed(wkv_calls(rnn)[name][0])

@@ -2,12 +2,14 @@
 stream may still be using what was freed on the host.  CPU only, with a stand-in for torch that
 notes the stream of each allocation."""
 import contextlib
+import sys
 import types
 
 import pytest
 
 pytest.importorskip("torch")
 from linear_rnn_sequence_amd import gated_delta as G  # noqa: E402
+from linear_rnn_sequence_amd import wkv as W  # noqa: E402
 
 
 class Stream:
@@ -84,3 +86,45 @@ def test_gated_delta_refuses_another_devices_stream():
     other = types.SimpleNamespace(type="cuda", index=1)
     with pytest.raises(ValueError, match="stream"):
         G._On(fake_torch(DEVICE, Stream(DEVICE, 1)), DEVICE, Stream(other, 2))
+
+
+def wkv_forward(monkeypatch, stream):
+    """A forward call on stand-ins: the stream of its readout, state and workspace, and its input r."""
+    real = pytest.importorskip("torch")
+    mine = Stream(DEVICE, 1)
+    torch = fake_torch(DEVICE, mine)
+    torch.bfloat16, torch.float32 = real.bfloat16, real.float32
+    seen = {}
+
+    def call(*args):
+        seen["stream"] = args[-1].value
+        return 0
+
+    lib = types.SimpleNamespace(rwkv7_wkv_forward=call, rwkv7_wkv_forward_workspace=lambda *a: 64)
+    monkeypatch.setitem(sys.modules, "torch", torch)
+    monkeypatch.setattr(W, "lib", lambda: lib)
+    monkeypatch.setattr(Memory, "data_ptr", lambda self: seen.setdefault(self.stream, []).append(self) or 16, raising=False)
+    monkeypatch.setattr(Memory, "numel", lambda self: 64, raising=False)
+    monkeypatch.setattr(Memory, "element_size", lambda self: 1, raising=False)
+    x = []
+    for _ in range(6):
+        t = Memory(mine)
+        t.shape, t.dtype, t.device = (2, 3, 4, 64), real.bfloat16, DEVICE
+        x.append(t)
+    y, s = W.forward(*x, stream=stream)
+    return seen, mine, x, y, s
+
+
+def test_wkv_memory_belongs_to_the_given_stream(monkeypatch):
+    side = Stream(DEVICE, 2)
+    seen, mine, x, y, s = wkv_forward(monkeypatch, side)
+    assert seen["stream"] == 2
+    assert len(seen[mine]) == 6 and len(seen[side]) == 3  # the inputs; readout, state and workspace
+    assert y.recorded == [mine] and s.recorded == [mine]
+    assert all(t.recorded == [side] for t in x)
+
+
+def test_wkv_memory_without_a_given_stream(monkeypatch):
+    seen, mine, x, y, s = wkv_forward(monkeypatch, None)
+    assert seen["stream"] == 1
+    assert len(seen[mine]) == 9 and not y.recorded and not x[0].recorded
