@@ -90,10 +90,8 @@ __device__ __forceinline__ void store_kept(const State<K> &s, E *state, int V, i
             *reinterpret_cast<u32x4 *>(at) = f.v;
             word[ks] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                word[ks] |= (__float_as_uint(a[e]) >> 12 & 15u) << 4 * e;
-                word[ks] |= (__float_as_uint(b[e]) >> 12 & 15u) << (16 + 4 * e);
-            }
+            for (int e = 0; e < 8; ++e)
+                word[ks] |= kept_code(__float_as_uint(e < 4 ? a[e] : b[e - 4])) << 4 * e;
         } else {
             *reinterpret_cast<f32x4 *>(at) = f.v[0];
             *reinterpret_cast<f32x4 *>(at + 4) = f.v[1];

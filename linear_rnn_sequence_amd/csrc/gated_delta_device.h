@@ -19,6 +19,7 @@
 // parts' products: the inputs q, k, v are bf16 and exact.
 #pragma once
 
+#include "gated_delta_kept.h"
 #include "wkv7_device.h"
 #include "wkv7_mfma.h"
 
@@ -328,21 +329,14 @@ struct Stage {
     }
 };
 
-// A stored state: [V, K] and, in bf16, four more bits of each element behind it (of its
-// float32's significand, those that follow the 16 bits that a truncation would keep).  A
-// word has eight elements', a row K / 8 words, those of the columns 32 ks + 8 g + .. at
-// g K / 32 + ks: so a lane of a chain kernel has its words side by side.  They are for
-// <S0, D>, a sum of V K products of either sign, of which rounded factors would leave
-// 2^-8 of their size, however small the sum.
+// A stored state: [V, K] and, in bf16, four more bits of each element behind it
+// (gated_delta_kept.h).  A word has eight elements', a row K / 8 words, those of the
+// columns 32 ks + 8 g + .. at g K / 32 + ks: so a lane of a chain kernel has its words
+// side by side.  They are for <S0, D>, a sum of V K products of either sign, of which
+// rounded factors would leave 2^-8 of their size, however small the sum.
 template <class E, int K>
 __device__ __forceinline__ size_t kept_size(int V) {
     return (size_t)V * (sizeof(E) == 2 ? K + K / 4 : K);
-}
-// a float from its rounding to bf16 (in the upper half of `hi`, the lower half 0) and its
-// code, the i-th of a word: where the bits say a half or more, the rounding went up
-__device__ __forceinline__ float kept_float(unsigned hi, unsigned word, int i) {
-    const int code = (int)(word << (28 - 4 * i)) >> 28;
-    return __uint_as_float((hi | 0x800u) + ((unsigned)code << 12));
 }
 
 // Stores a wave's 16 values of 64 tokens, which lie in result tiles [tokens, values],

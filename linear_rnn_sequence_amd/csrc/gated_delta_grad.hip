@@ -272,8 +272,9 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
                             const unsigned a = s[x >> 1], b = d[x >> 1];
-                            ds_sum += kept_float(x & 1 ? a & 0xffff0000u : a << 16, ms[i], x) *
-                                      kept_float(x & 1 ? b & 0xffff0000u : b << 16, md[i], x);
+                            const unsigned sb = kept_bits(x & 1 ? a & 0xffff0000u : a << 16, ms[i], x),
+                                           db = kept_bits(x & 1 ? b & 0xffff0000u : b << 16, md[i], x);
+                            ds_sum += __uint_as_float(sb) * __uint_as_float(db);
                         }
                     }
             }
