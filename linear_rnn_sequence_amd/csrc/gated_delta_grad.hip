@@ -7,7 +7,7 @@
 //   MP = dP * scale E,  MA = dA * beta E  (elementwise, beta of the row),
 //   dQ = scale diag(c) dO S0 + MP K,
 //   dK = -diag(beta c) dR S0 + diag(c_C / c) U D + MP^T Q + MA K + MA^T K,
-//   dbeta_t = dR_t . (v_t - c_t S0 k_t) + sum_s dA_ts E_ts k_t . k_s,
+//   dbeta_t = dR_t . (v_t - c_t S0 k_t) + sum_s dA_ts E_ts k_t . k_s = dR_t . U_t / beta_t,
 // and, since the decay at t lies on every path from a token before t (or from
 // the entry state) to a token at or behind t (or to the exit state),
 //   dg_t = sum_{s < t <= t'} (MP * q.k + MA * k.k)_{t's}
@@ -15,6 +15,14 @@
 //        + sum_{s < t} (c_C / c_s) U_s . D k_s + c_C <D, S0>,
 // a sum over a rectangle of pairs, in which nothing cancels (differences of row
 // and column sums of the same matrices would).
+//
+// The second form of dbeta is the diagonal of the product that dA is.  With e = U_t / beta_t
+// = v_t - r the error that the token corrects, r what the state recalls, and dR, U, S0
+// rounded (bf16), the first is off by d |dR| sqrt(|e|^2 + |r|^2) or so, the second by
+// d |dR| |e| sqrt(2), d = 2^-9.8 being a rounding in the mean.  Where the state recalls v well,
+// e is a small difference of v and r, of which the first form would leave little: tokens
+// with 2 |e|^2 < |v|^2 take the second one, the others the first, and |r| < 2.5 |e| there
+// (the first step's values tell the sizes well enough; all of them cost 9 us of 300).
 //
 // One workgroup of sixteen waves per chunk and key head; it goes through the value
 // heads that share the key head and adds their dq and dk up in registers, so no
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
     __shared__ __align__(16) float sBeta[kChunk], sRk[kChunk], sRq[kChunk];
     __shared__ float sGrown[kChunk], sRest[kChunk];
     __shared__ float sEntry[4][kChunk], sLeave[4][kChunk], sKS[4][kChunk], sDb[kChunk],
-        sDRV[kChunk], sPairs[kChunk], sDS[16];
+        sDRV[kChunk], sOwn[kChunk], sSize[2][kChunk], sPairs[kChunk], sDS[16];
 
     int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, lo = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -228,6 +236,10 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
         if (wave == 0 && lane < live) {
             gt = to_float(static_cast<const E *>(p.g)[gate_at]);
             bt = to_float(static_cast<const E *>(p.beta)[gate_at]);
+        }
+        {  // the sizes of U and v, from the first step's values
+            const float size = wkv7::sum_lanes8(dot_piece<E>(gb.x[0], gb.x[0], 0.f));
+            if ((tid & 7) == 0) sSize[upper][(tid & 511) >> 3] = size;
         }
         char *b0 = lds;
         for (int j = 0; j < steps; ++j) {
@@ -353,6 +365,11 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
         // the triangles: P becomes this part's operand, kq the pairs' terms of dg
         f32x4 pairs[4];
         if (part < 2) {  // the lane's token is t, rows are s
+            if (part) {  // dR_t . U_t: row t is in one lane of the token's four
+                const f32x4 a = w < 2 ? P[0] : P[2], b = w < 2 ? P[1] : P[3], x = lo & 4 ? b : a;
+                const float y = lo & 1 ? x[1] : x[0], z = lo & 1 ? x[3] : x[2];
+                if (g == (mine >> 3 & 3)) sOwn[mine] = lo & 2 ? z : y;
+            }
             float db = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -470,7 +487,12 @@ __global__ __launch_bounds__(kThreads) void gradient_kernel(GradArgs p) {
             if (lane < live) {
                 static_cast<E *>(p.dg)[gate_at] =
                     from_float<E>(sPairs[lane] + entry + (leave - own) + whole);
-                static_cast<E *>(p.dbeta)[gate_at] = from_float<E>(sDRV[lane] - ks + sDb[lane]);
+                // (a strength whose square, or U, may have lost bits below the smallest normal
+                // number takes the first form)
+                const float b = sBeta[lane];
+                const bool second = fabsf(b) > 0x1p-40f && 2.f * sSize[0][lane] < b * b * sSize[1][lane];
+                static_cast<E *>(p.dbeta)[gate_at] =
+                    from_float<E>(second ? sOwn[lane] / b : sDRV[lane] - ks + sDb[lane]);
             }
         }
         __syncthreads();  // before the next head's sums take their places
