@@ -20,10 +20,10 @@
 //
 // The state is float32 and what is added to it keeps 16 bits of significand or
 // more (split operands, gated_delta_device.h), so that s_out and ds0 are
-// float32 results; o is rounded to its type and takes U and P rounded to it, which together
-// make its error 1.6 times that of its own rounding.  (S0 rounded as well: 1.7 times for
-// 1% of a long prefill's time; U split as well: 1.35 times, but 2% more, for the split's
-// vector instructions.)
+// float32 results.  So does what enters o, but for P, which is rounded to o's type (its
+// other half would be 6 KB more of a chunk's record): o's error is 1.3 times that of its own
+// rounding.  With U rounded as well it was 1.6 times that, and the pass took 1 to 2% less
+// (16 ragged sequences 197 us for 202, 32768 tokens 788 for 798).
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
@@ -486,14 +486,18 @@ __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_
             // the readout: O^T += U^T P^T
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                const Frag<E> b = to_frag<E>(U[2 * st], U[2 * st + 1]);
+                const Split<E> b = to_split<E>(U[2 * st], U[2 * st + 1]);
+                if constexpr (L::kRecord)
 #pragma unroll
-                for (int f = 0; f < 6; ++f)
-                    if (kLowStep[f] == st) {
-                        if constexpr (L::kRecord)
+                    for (int f = 0; f < 6; ++f)
+                        if (kLowStep[f] == st)
                             P[f] = get_frag<E>(rc + Rec::kP + f * Rec::kFragBytes, lane);
-                        O[kLowTile[f]] = mma(b, P[f], O[kLowTile[f]]);
-                    }
+#pragma unroll
+                for (int part = 0; part < kPartsMixed<E>; ++part)
+#pragma unroll
+                    for (int f = 0; f < 6; ++f)
+                        if (kLowStep[f] == st)
+                            O[kLowTile[f]] = mma_mixed(part, b, P[f], O[kLowTile[f]]);
             }
             if constexpr (L::kShared) {  // in the place of the values
 #pragma unroll
