@@ -40,6 +40,9 @@ struct MoveArgs {
 
 __global__ __launch_bounds__(kThreads) void state_move_kernel(MoveArgs p) {
     __shared__ int sKey[kTable], sLast[kTable];
+    // the pairs as they were read once (targets out of range: -1): were they read again for the
+    // search below, a list that is written meanwhile would make it look for what is not there
+    __shared__ int sSrc[kMax], sDst[kMax];
     const int tid = threadIdx.x;
     for (int i = tid; i < kTable; i += kThreads) {
         sKey[i] = -1;
@@ -50,6 +53,8 @@ __global__ __launch_bounds__(kThreads) void state_move_kernel(MoveArgs p) {
     auto hash = [](int d) { return (int)(((unsigned)d * 2654435761u) >> 16) & (kTable - 1); };
     for (int i = tid; i < p.n; i += kThreads) {
         const int s = p.src[i], d = p.dst[i];
+        sSrc[i] = s;
+        sDst[i] = valid(s, d) ? d : -1;
         if (!valid(s, d)) continue;
         int h = hash(d);
         // ends: at most kMax of the kTable places are ever taken
@@ -69,8 +74,8 @@ __global__ __launch_bounds__(kThreads) void state_move_kernel(MoveArgs p) {
         const int i = row0 + j * rows;
         from[j] = to[j] = -1;
         if (i >= p.n) continue;
-        const int s = p.src[i], d = p.dst[i];
-        if (!valid(s, d)) continue;
+        const int s = sSrc[i], d = sDst[i];
+        if (d < 0) continue;
         int h = hash(d);
         while (sKey[h] != d) h = (h + 1) & (kTable - 1);  // it was put there above
         if (sLast[h] != i) continue;

@@ -238,3 +238,11 @@ def test_stored_states_need_the_bits_behind_them():
     with pytest.raises(ValueError):  # the same rows, further on in the memory
         G._check_ckpt(torch, whole.as_strided((2, *tail), strides, 2 * size + 128), 2, tail, torch.bfloat16, cpu)
     G._check_ckpt(torch, torch.zeros(chunks, *tail), chunks, tail, torch.float32, cpu)
+
+
+def test_moves_read_each_pair_once():
+    """The kernel searches a table for the targets it has put there; a second read of the list, written meanwhile,
+    could give one that is not, and the search would not end."""
+    src = re.sub(r"//.*", "", open(os.path.join(hbuild.CSRC, "state_move.hip")).read())
+    for name in ("src", "dst"):
+        assert len(re.findall(rf"\bp\.{name}\[", src)) == 1, name
