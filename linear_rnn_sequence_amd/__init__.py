@@ -3,7 +3,7 @@ behind a C ABI (include/rwkv7_wkv.h, include/gated_delta.h), with this package a
 binding."""
 from .gated_delta import (STATE_MOVE_MAX, gated_delta_backward,  # noqa: F401
                           gated_delta_backward_workspace_bytes, gated_delta_chunks,
-                          gated_delta_decode, gated_delta_forward,
+                          gated_delta_ckpt_size, gated_delta_decode, gated_delta_forward,
                           gated_delta_forward_train, gated_delta_forward_workspace_bytes,
                           state_move)
 from .wkv import (ALGOS, CKPT_INTERVAL, Rwkv7Error, abi_version, backward,  # noqa: F401

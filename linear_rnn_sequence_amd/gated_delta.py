@@ -103,9 +103,11 @@ def _ckpt_size(torch, V, K, dtype):
 
 def _check_ckpt(torch, t, chunks, tail, dtype, device):
     """The states that the training forward stores: [chunks,Hv,V,K], GATED_DELTA_CKPT_SIZE apart with the
-    further bits behind each, the last one as well."""
+    further bits behind each, the last one as well; or all of it as [chunks,Hv,GATED_DELTA_CKPT_SIZE]."""
     Hv, V, K = tail
     size = _ckpt_size(torch, V, K, dtype)
+    if t.dim() == 3:
+        return _dense(t, "s_ckpt", (chunks, Hv, size), dtype, device)
     if t.shape != (chunks, *tail) or t.dtype != dtype or t.device != device:
         raise ValueError(f"s_ckpt: {tuple(t.shape)} {t.dtype} on {t.device}, expected {(chunks, *tail)} {dtype} "
                          f"on {device}")
@@ -254,6 +256,11 @@ def gated_delta_chunks(tokens, *, sequences=1, packed=False) -> int:
     return _query("gated_delta_chunks", tokens, 1, 1, 64, 64, sequences, packed, "bf16")
 
 
+def gated_delta_ckpt_size(V, K, *, dtype="bf16") -> int:
+    """Elements of one stored state (GATED_DELTA_CKPT_SIZE): V K, and in bf16 V K / 4 for its further bits."""
+    return V * K + (V * K // 4 if _wkv._dtype_name_code(dtype) == DT_BF16 else 0)
+
+
 def gated_delta_forward(q, k, v, g, beta, s0=None, *, cu_seqlens=None, slots=None, slots_in=None,
                         scale=None, normalize=False, o=None, s_out=None, want_state=True,
                         workspace=None, stream=None):
@@ -331,8 +338,10 @@ def gated_delta_forward_train(q, k, v, g, beta, s0=None, *, cu_seqlens=None, sca
                               normalize=False, o=None, s_out=None, want_state=True, s_ckpt=None,
                               u=None, workspace=None, stream=None):
     """gated_delta_forward_train.  Returns (o, s_out, s_ckpt, u); s_ckpt [chunks,Hv,V,K] and u (like
-    v), in the inputs' dtype, are what :func:`gated_delta_backward` needs besides the inputs (bf16
-    states have further bits behind each, which a copy of the tensor would lose: it is refused)."""
+    v), in the inputs' dtype, are what :func:`gated_delta_backward` needs besides the inputs.  bf16
+    states have further bits behind each, which a copy of that view would lose (it is refused).  To
+    move or copy them meanwhile (activation offload, hooks on saved tensors), give ``s_ckpt`` as a tensor
+    [chunks,Hv,:func:`gated_delta_ckpt_size`], which holds them too and which the backward takes as well."""
     import torch
 
     _check_ranks(q, k, v, g, beta)

@@ -246,3 +246,19 @@ def test_moves_read_each_pair_once():
     src = re.sub(r"//.*", "", open(os.path.join(hbuild.CSRC, "state_move.hip")).read())
     for name in ("src", "dst"):
         assert len(re.findall(rf"\bp\.{name}\[", src)) == 1, name
+
+
+@pytest.mark.parametrize("dtype,name", [(torch.bfloat16, "bf16"), (torch.float32, "f32")])
+def test_stored_states_as_one_dense_tensor(dtype, name):
+    """[chunks, Hv, GATED_DELTA_CKPT_SIZE], which may be copied; other sizes, types and layouts are refused."""
+    cpu, tail, chunks = torch.device("cpu"), (2, 64, 128), 3
+    size = rnn.gated_delta_ckpt_size(64, 128, dtype=name)
+    assert size == G._ckpt_size(torch, 64, 128, dtype)
+    good = torch.zeros(chunks, 2, size, dtype=dtype)
+    G._check_ckpt(torch, good, chunks, tail, dtype, cpu)
+    G._check_ckpt(torch, good.clone(), chunks, tail, dtype, cpu)
+    for bad in (good[1:], good[:, :1], good[..., :-1], good.transpose(0, 1), torch.zeros(chunks, 2, size + 4, dtype=dtype)):
+        with pytest.raises(ValueError):
+            G._check_ckpt(torch, bad, chunks, tail, dtype, cpu)
+    with pytest.raises(TypeError):
+        G._check_ckpt(torch, good.half(), chunks, tail, dtype, cpu)
