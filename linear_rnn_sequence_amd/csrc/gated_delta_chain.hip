@@ -196,12 +196,12 @@ struct ForwardLds {
 // accesses out of range.
 //
 // What bounds it: a chunk of 128 keys and 128 values (eight waves, one workgroup per
-// CU) takes about 8000 cycles, of which shared memory is busy 4400, a SIMD's matrix
-// core 3300 and its vector units 3100; the products depend on each other, and two
-// waves per SIMD, of 256 registers each, do not overlap them fully.  16 sequences of
-// up to 2049 tokens and 32 heads take 138 us, as long as the longest one's chunks
-// one after the other.  With 64 keys and values (8 x 4096 tokens, 40 heads: 317 us)
-// it is memory: 1.07 GB with the records, 3.4 TB/s, at most one chunk ahead.
+// CU) takes about 8200 cycles, of which shared memory is busy 55% (20% bank conflicts),
+// a SIMD's matrix core 49% and its vector units 42%; the products depend on each other,
+// and two waves per SIMD, of 256 registers each, do not overlap them fully.  16 sequences
+// of up to 2049 tokens and 32 heads take 141 us, as long as the longest one's chunks
+// one after the other.  With 64 keys and values (8 x 4096 tokens, 40 heads: 318 us)
+// it is memory: 1.08 GB with the records, 3.4 TB/s, at most one chunk ahead.
 //
 // A workgroup takes a whole sequence, or one segment of it (p.seg): kSummary only
 // carries the state over a segment, from zeros (from the sequence's state for its
@@ -209,7 +209,7 @@ struct ForwardLds {
 // rows of the unit matrix and see no values, which gives the segment's
 // transition S0 -> S0 M.  combine_kernel turns these into the states at the
 // segments' starts, from which the segments are then done in parallel (32768 tokens, 32
-// heads of 128 x 128, eight segments: 330, 25 and 272 us).
+// heads of 128 x 128, eight segments: 325, 25 and 277 us).
 template <class E, int K, int W, Mode MODE>
 __global__ __launch_bounds__(64 * W, sizeof(E) == 2 ? 2 : 1) void forward_chain_kernel(
     ChainArgs p) {
@@ -640,7 +640,7 @@ struct BackwardLds {
 // The same pipeline backwards: the rows of k and q and the record double-buffered; where
 // that does not fit (float, 128 keys) T^T and P^T are loaded again as soon as they have been
 // used.  It is bound by the length of the chain of products, one wave per SIMD: 4 x 2048
-// tokens, 32 heads of 128 x 128, take 167 us, 5.2 us a chunk, where the matrix cores are
+// tokens, 32 heads of 128 x 128, take 163 us, 5.1 us a chunk, where the matrix cores are
 // busy 1 us (26 us more before the parts of split products were interleaved, mma_mixed).
 template <class E, int K>
 __global__ __launch_bounds__(kThreads, 1) void backward_chain_kernel(ChainArgs p) {
@@ -918,7 +918,11 @@ ChainArgs chain_args(const Problem &p) {
 // segments' summaries costs about what the pass over them does, so there have to be
 // four segments a sequence, long enough for the launches: 8 heads of 128 values,
 // two sequences of up to 1001 tokens took 102 us whole and 54 us in segments (float), 34 us
-// either way with 128 tokens a segment in bf16, which has shorter chunks.
+// either way with 128 tokens a segment in bf16, which has shorter chunks.  The rule
+// goes by the average length, which the host knows also of a packed batch, and does not
+// weigh the combination, whose steps follow each other: a long sequence among many short
+// ones is done whole, and the more segments a single one has, the longer is that part (4 us
+// a step with 128 keys).
 Segments plan_segments(const Problem &p) {
     Segments s{};
     s.units = p.n_seq;

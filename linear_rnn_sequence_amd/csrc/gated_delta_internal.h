@@ -40,7 +40,7 @@ struct BackwardArgs {
     void *dq, *dk, *dv, *dg, *dbeta;
     float *ds0;
     char *records;  // workspace: T^T, P^T and scalars of every chunk and value head
-    void *ds;       // workspace: [slots, Hv, V, K], cotangent of each chunk's exit state
+    void *ds;       // workspace: [slots, Hv, GATED_DELTA_CKPT_SIZE], cotangent of each chunk's exit state
     void *dr;       // workspace: [total, Hv, V]
 };
 

@@ -25,9 +25,10 @@
 // decays.  So outside the diagonal blocks E_ts is a product of two numbers, from s
 // to the end of its block of 16 and from there to t (both at most 1), of which
 // there are few: a table per value head, with the other factors of t and of s in it
-// (32768 tokens, 16 key heads of two value heads, K = 128: 165 us without the tables, 141 us
-// with them, 4.2 TB/s of rows and records; 8 x 4096 tokens of 40 heads, K = 64: 196 us).
-// Four workgroups a CU: with the registers for five, 300 us in place of those 196.
+// (32768 tokens, 16 key heads of two value heads, K = 128: 165 us without the tables, 143 us
+// with them, 4.3 TB/s of rows and records; 8 x 4096 tokens of 40 heads, K = 64: 200 us).
+// Vector units are busy 50 to 60% of the time, the waves wait half of theirs.
+// Four workgroups a CU: with the registers for five, 300 us in place of those 200.
 #include "gated_delta_device.h"
 #include "gated_delta_internal.h"
 
