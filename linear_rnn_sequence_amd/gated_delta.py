@@ -65,6 +65,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _counts(**counts):
+    """Refuses numbers that the C interface's ints do not hold (ctypes would cut them off)."""
+    for name, n in counts.items():
+        if not 0 <= n < 1 << 31:
+            raise ValueError(f"{name}: {n} is not below 2^31")
+
+
 def _token_stride(x, name, lead, H, C):
     """Elements from one token's channels to the next's (0: dense) of x [*lead, H, C]."""
     shape = (*lead, H, C)
@@ -147,12 +154,15 @@ def _problem(torch, q, k, v, g, beta, cu_seqlens, slots_in, slots_out, pool, sca
     n = lead[0]
     total = n * lead[1] if len(lead) == 2 else n
     cu = None
+    if total >> 31:
+        _counts(tokens=total)
     if cu_seqlens is not None:
         if n != 1:
             raise ValueError("a packed batch has B = 1")
         n = cu_seqlens.numel() - 1
         if n < 1:
             raise ValueError("cu_seqlens holds n + 1 offsets of n >= 1 sequences")
+        _counts(sequences=n)
         cu = _index(torch, cu_seqlens, "cu_seqlens", n + 1, dev)
     into = _index(torch, slots_out, "slots", n, dev)
     start = into if slots_in is slots_out else _index(torch, slots_in, "slots_in", n, dev)
@@ -232,6 +242,7 @@ class _On:
 
 
 def _query(name, tokens, Hk, Hv, K, V, sequences, packed, dtype):
+    _counts(tokens=tokens, Hk=Hk, Hv=Hv, K=K, V=V, sequences=sequences)
     p = Problem(n_seq=sequences, total=tokens, Hk=Hk, Hv=Hv, K=K, V=V, pool=sequences,
                 dt=_wkv._dtype_name_code(dtype))
     if packed:
@@ -433,6 +444,7 @@ def state_move(pool, src, dst, *, slot_dim=0, stream=None):
     for d in pool.shape[slot_dim + 1:]:
         size *= d
     n = src.numel()
+    _counts(layers=layers, slots=slots, pairs=n)
     _index(torch, src, "src", n, dev)
     _index(torch, dst, "dst", n, dev)
     step = pool.stride(0) * pool.element_size() if slot_dim and layers > 1 else 0

@@ -262,3 +262,48 @@ def test_stored_states_as_one_dense_tensor(dtype, name):
             G._check_ckpt(torch, bad, chunks, tail, dtype, cpu)
     with pytest.raises(TypeError):
         G._check_ckpt(torch, good.half(), chunks, tail, dtype, cpu)
+
+
+class Wide:
+    """A tensor of any size, without its memory."""
+
+    def __init__(self, shape, dtype=torch.float32):
+        self.shape, self.dtype, self.device = shape, dtype, torch.device("cuda", 0)
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        n = 1
+        for d in self.shape:
+            n *= d
+        return n
+
+    def element_size(self):
+        return 4 if self.dtype == torch.float32 else 2
+
+    def data_ptr(self):
+        raise AssertionError("refused before")
+
+
+def test_numbers_that_do_not_fit_an_int_are_refused():
+    """2^32 + 4 slots of 16 bytes would be 4 to the library, 2^32 + 1 sequences one."""
+    pair = Wide((2,), torch.int32)
+    for shape, dim in (((2 ** 32 + 4, 4), 0), ((1, 2 ** 32 + 4, 4), 1), ((2 ** 32 + 1, 2, 4), 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            rnn.state_move(Wide(shape), pair, pair, slot_dim=dim)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rnn.state_move(Wide((4, 4)), Wide((2 ** 32 + 1,), torch.int32), Wide((2 ** 32 + 1,), torch.int32))
+    bf = torch.bfloat16
+    for T, n in ((2 ** 32 + 64, 2), (64, 2 ** 32 + 1)):
+        q, v, g = Wide((1, T, 1, 64), bf), Wide((1, T, 1, 64), bf), Wide((1, T, 1), bf)
+        with pytest.raises(ValueError, match="2\\^31"):
+            rnn.gated_delta_forward(q, q, v, g, g, cu_seqlens=Wide((n + 1,), torch.int32), want_state=False)
+    for f in (rnn.gated_delta_forward_workspace_bytes, rnn.gated_delta_backward_workspace_bytes):
+        with pytest.raises(ValueError, match="2\\^31"):
+            f(2 ** 32 + 64, 1, 1, 64, 64)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rnn.gated_delta_chunks(2 ** 33)
