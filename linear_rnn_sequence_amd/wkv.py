@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the recurrence runs in the HIP
 kernels of the library.  torch provides device memory and the stream; the
 functions take CUDA (HIP) tensors and pass their data pointers and
-``torch.cuda.current_stream().cuda_stream`` (unless a stream is given).
+``torch.cuda.current_stream().cuda_stream`` (unless a stream is given: it does not
+wait for the current one, nor the other way round, but memory on both sides is safe
+to free at any time).
 
 There is no CPU fallback: if the library is not built, :func:`lib` raises.
 """
