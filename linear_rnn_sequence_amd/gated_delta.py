@@ -68,7 +68,7 @@ def _ptr(t):
 def _counts(**counts):
     """Refuses numbers that the C interface's ints do not hold (ctypes would cut them off)."""
     for name, n in counts.items():
-        if not 0 <= n < 1 << 31:
+        if n >= 1 << 31:
             raise ValueError(f"{name}: {n} is not below 2^31")
 
 

@@ -307,3 +307,4 @@ def test_numbers_that_do_not_fit_an_int_are_refused():
             f(2 ** 32 + 64, 1, 1, 64, 64)
     with pytest.raises(ValueError, match="2\\^31"):
         rnn.gated_delta_chunks(2 ** 33)
+    assert rnn.gated_delta_forward_workspace_bytes(-1, 1, 1, 64, 64) == 0  # invalid, as other sizes that are none
