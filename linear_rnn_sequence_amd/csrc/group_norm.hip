@@ -1,0 +1,536 @@
+// Group norm of rows with an activation or gate, forward and backward (include/group_norm.h).
+//
+// A team of L lanes (a power of two) has one group of one row: each lane NV pieces of VEC
+// elements, the lanes' pieces side by side, so that neighbouring teams, which have
+// neighbouring groups, read whole lines.  The group lies in registers: mean, then the
+// variance from the differences to it, then the output, with one read and one write of
+// memory.  Sums over the team are DPP moves and lane swaps.
+//
+// Forward: y = n act(gate) or act(n), n = u w + b, u = (x - mean) rstd.
+// Backward, with the same values formed again from x:
+//   dn = dy act(gate) or dy act'(n),  dgate = dy n act'(gate),  du = dn w,
+//   dx = rstd (du - mean(du) - u mean(du u)),   dw = sum over rows of dn u,  db = of dn.
+// A team keeps its group for several rows, whose sums of dw and db it writes as one row of the
+// workspace; sum_kernel adds those in a fixed order.
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "group_norm.h"
+#include "wkv7_device.h"
+#include "wkv7_mfma.h"
+
+namespace gnorm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSize = 1024;
+
+struct Args {
+    const void *x, *gate, *dy;
+    const float *weight, *bias;
+    void *y, *dx, *dgate;
+    float *sums;  // [chunks, 2, C]
+    long long rows, x_stride, gate_stride;
+    int groups, size, act, per_team;  // per_team: rows of a team
+    float eps, inv_size;
+    bool rms;
+};
+
+// sum over the L lanes of a team, in all of them
+template <int L>
+__device__ __forceinline__ float team_sum(float x) {
+    x = L == 8 ? wkv7::sum_lanes8(x) : wkv7::sum_lanes16(x);
+    if constexpr (L >= 32) x = wkv7::swap16_add(x, x);
+    if constexpr (L >= 64) x = wkv7::swap32_add(x, x);
+    return x;
+}
+
+// VEC elements of type E as they lie in memory
+template <class E, int VEC>
+struct alignas(sizeof(E) * VEC) Raw {
+    E e[VEC];
+};
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+template <int VEC>
+__device__ __forceinline__ void narrow(Raw<uint16_t, VEC> &r, const float (&x)[VEC]) {
+    if constexpr (VEC == 1) {
+        r.e[0] = (uint16_t)wkv7::f32_to_bf16_rne(x[0]);
+    } else {
+        unsigned u[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) u[i] = wkv7::cvt_pk(x[2 * i], x[2 * i + 1]);
+        __builtin_memcpy(&r, u, sizeof(r));
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void narrow(Raw<float, VEC> &r, const float (&x)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.e[i] = x[i];
+}
+
+// sigmoid; for outputs of 8 bits the hardware's exponential and reciprocal, 2^-22 off
+template <class E>
+__device__ __forceinline__ float sigmoid(float x) {
+    if constexpr (sizeof(E) == 2)
+        return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+    return 1.f / (1.f + expf(-x));
+}
+template <class E>
+__device__ __forceinline__ float activate(float x, int act) {
+    if (act == GROUP_NORM_NONE) return x;
+    const float s = sigmoid<E>(x);
+    return act == GROUP_NORM_SILU ? x * s : s;
+}
+// the activation, and its derivative
+template <class E>
+__device__ __forceinline__ float activate(float x, int act, float &slope) {
+    slope = 1.f;
+    if (act == GROUP_NORM_NONE) return x;
+    const float s = sigmoid<E>(x);
+    slope = act == GROUP_NORM_SILU ? s + x * (s - s * s) : s - s * s;
+    return act == GROUP_NORM_SILU ? x * s : s;
+}
+
+// Which group, and which rows, a thread's team has; the lane's number in the team.
+template <int L>
+struct Place {
+    int group, lane;
+    long long first, end;  // rows
+    __device__ __forceinline__ Place(const Args &a) {
+        const unsigned team = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / L;
+        lane = (int)(threadIdx.x % L);
+        group = (int)(team % (unsigned)a.groups);
+        first = (long long)(team / (unsigned)a.groups) * a.per_team;
+        end = first + a.per_team < a.rows ? first + a.per_team : a.rows;
+    }
+};
+
+// the statistics of R rows at once, one chain of sums beside the other: afterwards x holds u
+template <int L, int N, int R>
+__device__ __forceinline__ void normalize(float (&x)[R][N], float (&rstd)[R], const bool (&has)[N],
+                                          const Args &a) {
+    float mean[R], var[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mean[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) mean[r] += x[r][i];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] = a.rms ? 0.f : team_sum<L>(mean[r]) * a.inv_size;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        var[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[r][i] = has[i] ? x[r][i] - mean[r] : 0.f;
+            var[r] += x[r][i] * x[r][i];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rstd[r] = 1.f / sqrtf(team_sum<L>(var[r]) * a.inv_size + a.eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[r][i] *= rstd[r];
+    }
+}
+
+template <class E, int VEC, int L, int NV, int R, bool GATE>
+__global__ __launch_bounds__(kThreads) void forward_kernel(Args a) {
+    constexpr int N = VEC * NV;
+    using V = Raw<E, VEC>;
+    const Place<L> at(a);
+    if (at.first >= a.rows) return;
+    const int pieces = a.size / VEC;
+    bool has[N];
+    int col[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int piece = v * L + at.lane;
+        col[v] = at.group * a.size + (piece < pieces ? piece : 0) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = piece < pieces;
+    }
+    const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate);
+    const long long C = (long long)a.groups * a.size;
+    V rx[R][NV], rg[R][NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const long long row = at.first + r < at.end ? at.first + r : at.first;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            rx[r][v] = *reinterpret_cast<const V *>(xp + row * a.x_stride + col[v]);
+            if constexpr (GATE) rg[r][v] = *reinterpret_cast<const V *>(gp + row * a.gate_stride + col[v]);
+        }
+    }
+    float w[N], b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        w[i] = a.weight ? a.weight[col[i / VEC] + i % VEC] : 1.f;
+        b[i] = a.bias ? a.bias[col[i / VEC] + i % VEC] : 0.f;
+    }
+    float u[R][N], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[r][i] = has[i] ? widen(rx[r][i / VEC].e[i % VEC]) : 0.f;
+    normalize<L, N, R>(u, rstd, has, a);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (at.first + r >= at.end) break;
+        E *yp = static_cast<E *>(a.y) + (at.first + r) * C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float y[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int k = v * VEC + i;
+                const float n = u[r][k] * w[k] + b[k];
+                if constexpr (GATE)
+                    y[i] = n * activate<E>(widen(rg[r][v].e[i]), a.act);
+                else
+                    y[i] = activate<E>(n, a.act);
+            }
+            if (has[v * VEC]) {
+                V out;
+                narrow(out, y);
+                *reinterpret_cast<V *>(yp + col[v]) = out;
+            }
+        }
+    }
+}
+
+template <class E, int VEC, int L, int NV, bool GATE>
+__global__ __launch_bounds__(kThreads) void backward_kernel(Args a) {
+    constexpr int N = VEC * NV;
+    using V = Raw<E, VEC>;
+    const Place<L> at(a);
+    if (at.first >= a.rows) return;
+    const int pieces = a.size / VEC;
+    bool has[N];
+    int col[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int piece = v * L + at.lane;
+        col[v] = at.group * a.size + (piece < pieces ? piece : 0) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = piece < pieces;
+    }
+    const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate),
+            *dp = static_cast<const E *>(a.dy);
+    const long long C = (long long)a.groups * a.size;
+    float w[N], b[N], dw[N], db[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        w[i] = a.weight ? a.weight[col[i / VEC] + i % VEC] : 1.f;
+        b[i] = a.bias ? a.bias[col[i / VEC] + i % VEC] : 0.f;
+        dw[i] = db[i] = 0.f;
+    }
+    V rx[NV], rg[NV], rd[NV];
+    auto fetch = [&](long long row) {
+        if (row >= at.end) row = at.end - 1;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            rx[v] = *reinterpret_cast<const V *>(xp + row * a.x_stride + col[v]);
+            rd[v] = *reinterpret_cast<const V *>(dp + row * C + col[v]);
+            if constexpr (GATE) rg[v] = *reinterpret_cast<const V *>(gp + row * a.gate_stride + col[v]);
+        }
+    };
+    fetch(at.first);
+    for (long long row = at.first; row < at.end; ++row) {
+        float u[1][N], rstd[1], gate[N], dy[N], dn[N], dz[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            u[0][i] = has[i] ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
+            dy[i] = has[i] ? widen(rd[i / VEC].e[i % VEC]) : 0.f;
+            if constexpr (GATE) gate[i] = widen(rg[i / VEC].e[i % VEC]);
+        }
+        if (row + 1 < at.end) fetch(row + 1);  // (dx may be dy: not this row's again)
+        normalize<L, N, 1>(u, rstd, has, a);
+        float sum = 0.f, along = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float n = u[0][i] * w[i] + b[i];
+            float slope;
+            if constexpr (GATE) {
+                const float act = activate<E>(gate[i], a.act, slope);
+                dn[i] = dy[i] * act;
+                dz[i] = dy[i] * n * slope;
+            } else {
+                activate<E>(n, a.act, slope);
+                dn[i] = dy[i] * slope;
+            }
+            dw[i] += dn[i] * u[0][i];
+            db[i] += dn[i];
+            dn[i] = has[i] ? dn[i] * w[i] : 0.f;
+            sum += dn[i];
+            along += dn[i] * u[0][i];
+        }
+        sum = a.rms ? 0.f : team_sum<L>(sum) * a.inv_size;
+        along = team_sum<L>(along) * a.inv_size;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float d[VEC], z[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int k = v * VEC + i;
+                d[i] = rstd[0] * (dn[k] - sum - u[0][k] * along);
+                if constexpr (GATE) z[i] = dz[k];
+            }
+            if (has[v * VEC]) {
+                V out;
+                narrow(out, d);
+                *reinterpret_cast<V *>(static_cast<E *>(a.dx) + row * C + col[v]) = out;
+                if constexpr (GATE) {
+                    narrow(out, z);
+                    *reinterpret_cast<V *>(static_cast<E *>(a.dgate) + row * C + col[v]) = out;
+                }
+            }
+        }
+    }
+    if (a.sums) {
+        float *s = a.sums + at.first / a.per_team * 2 * C;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (has[i]) {
+                s[col[i / VEC] + i % VEC] = dw[i];
+                s[C + col[i / VEC] + i % VEC] = db[i];
+            }
+    }
+}
+
+// out[c] = sum over the chunks' rows of column c (a chunk: [2, C], dweight's and dbias')
+__global__ __launch_bounds__(1024) void sum_kernel(const float *sums, float *dweight, float *dbias,
+                                                   int chunks, int C) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long c = (long long)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < 2LL * C)
+        for (long long i = wave; i < chunks; i += 16) s += sums[i * 2 * C + c];
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < 2LL * C) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += part[i][lane];
+        if (c < C) {
+            if (dweight) dweight[c] = s;
+        } else if (dbias) {
+            dbias[c - C] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+struct Shape {
+    int L, nv;  // lanes of a team, 8 to 64, and pieces of a lane, both powers of two
+};
+Shape shape_of(int size, int vec) {
+    const int pieces = size / vec;
+    Shape s{8, 1};
+    while (s.L < 64 && s.L < pieces) s.L *= 2;
+    while (s.L * s.nv < pieces) s.nv *= 2;
+    return s;
+}
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+struct Checked {
+    Args a;
+    int esz;
+};
+rwkv7_status check_problem(const group_norm_problem *in, Checked &c) {
+    if (!in) return RWKV7_ERR_NULL;
+    if (in->dt != RWKV7_DT_F32 && in->dt != RWKV7_DT_BF16)
+        return in->dt == RWKV7_DT_BF16_W32 ? RWKV7_ERR_UNSUPPORTED : RWKV7_ERR_DTYPE;
+    if (in->activation < GROUP_NORM_NONE || in->activation > GROUP_NORM_SIGMOID || in->size > kMaxSize)
+        return RWKV7_ERR_UNSUPPORTED;
+    if (in->rows < 0 || in->rows > 0x7fffffffLL || in->groups < 1 || in->size < 1) return RWKV7_ERR_SHAPE;
+    const long long C = (long long)in->groups * in->size, limit = 1LL << 23;
+    const long long xs = in->x_stride ? in->x_stride : C, gs = in->gate_stride ? in->gate_stride : C;
+    // (rows and strides below 2^31 and 2^23, so that bytes fit 64 bits by far)
+    if (C > limit || xs < C || gs < C || xs > limit || gs > limit) return RWKV7_ERR_SHAPE;
+    c.a = Args{};
+    c.a.rows = in->rows; c.a.groups = in->groups; c.a.size = in->size;
+    c.a.x_stride = xs; c.a.gate_stride = gs;
+    c.a.eps = in->eps; c.a.inv_size = 1.f / (float)in->size;
+    c.a.act = in->activation;
+    c.a.rms = in->rms != 0;
+    c.esz = in->dt == RWKV7_DT_BF16 ? 2 : 4;
+    return RWKV7_OK;
+}
+
+// Rows of a team in the backward: few enough that the teams fill the card several times over,
+// so many that the sums they leave are few bytes beside the rows.
+int backward_rows(const Args &a) {
+    const Shape s = shape_of(a.size, 1);
+    const long long teams = 4096LL * 64 / (s.L < 8 ? 8 : s.L);  // of about eight waves a SIMD
+    long long n = a.rows * a.groups / teams;
+    n = n < 8 ? 8 : n > 64 ? 64 : n;
+    return (int)n;
+}
+long long chunks_of(const Args &a, int per_team) { return (a.rows + per_team - 1) / per_team; }
+
+size_t extent(long long rows, long long stride, long long C, int esz) {
+    return rows ? (size_t)((rows - 1) * stride + C) * esz : 0;
+}
+
+struct Range {
+    const void *p;
+    size_t bytes;
+};
+bool overlap(Range a, Range b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range *a = outs.begin(); a != outs.end(); ++a) {
+        for (const Range *b = a + 1; b != outs.end(); ++b)
+            if (overlap(*a, *b)) return false;
+        for (const Range &b : ins)
+            if (overlap(*a, b)) return false;
+    }
+    return true;
+}
+
+// Elements of a piece: 16 bytes, or two of 16 bits, or one, as group, strides and addresses allow.
+int piece(const Args &a, int esz, std::initializer_list<const void *> ps) {
+    auto fits = [&](int vec) {
+        if (a.size % vec || a.x_stride % vec || (a.gate && a.gate_stride % vec)) return false;
+        for (const void *p : ps)
+            if (!aligned(p, (size_t)vec * esz)) return false;
+        return true;
+    };
+    return fits(16 / esz) ? 16 / esz : esz == 2 && fits(2) ? 2 : 1;
+}
+
+template <class E, int VEC, int L, int NV>
+hipError_t launch(Args a, bool backward, hipStream_t stream) {
+    // several rows of a team at once where there are teams enough without
+    constexpr int R = NV == 1 ? 4 : NV == 2 ? 2 : 1;
+    const bool many = R > 1 && a.rows * a.groups * L >= 64LL * 8192;
+    void (*kernel)(Args);
+    if (backward)
+        kernel = a.gate ? &backward_kernel<E, VEC, L, NV, true> : &backward_kernel<E, VEC, L, NV, false>;
+    else if (many)
+        kernel = a.gate ? &forward_kernel<E, VEC, L, NV, R, true> : &forward_kernel<E, VEC, L, NV, R, false>;
+    else
+        kernel = a.gate ? &forward_kernel<E, VEC, L, NV, 1, true> : &forward_kernel<E, VEC, L, NV, 1, false>;
+    a.per_team = backward ? backward_rows(a) : many ? R : 1;
+    const long long teams = chunks_of(a, a.per_team) * a.groups;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((teams * L + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+template <class E, int VEC>
+hipError_t launch(const Args &a, bool backward, hipStream_t stream) {
+    const Shape s = shape_of(a.size, VEC);
+    if (s.L == 8) return launch<E, VEC, 8, 1>(a, backward, stream);
+    if (s.L == 16) return launch<E, VEC, 16, 1>(a, backward, stream);
+    if (s.L == 32) return launch<E, VEC, 32, 1>(a, backward, stream);
+    if (s.nv == 1) return launch<E, VEC, 64, 1>(a, backward, stream);
+    if (s.nv == 2) return launch<E, VEC, 64, 2>(a, backward, stream);
+    if constexpr (VEC <= 4)
+        if (s.nv == 4) return launch<E, VEC, 64, 4>(a, backward, stream);
+    if constexpr (VEC <= 2)
+        if (s.nv == 8) return launch<E, VEC, 64, 8>(a, backward, stream);
+    if constexpr (VEC == 1)
+        if (s.nv == 16) return launch<E, VEC, 64, 16>(a, backward, stream);
+    return hipErrorInvalidValue;
+}
+hipError_t launch(const Args &a, int esz, int vec, bool backward, hipStream_t stream) {
+    if (a.rows == 0) return hipSuccess;
+    if (esz == 4) return vec == 4 ? launch<float, 4>(a, backward, stream) : launch<float, 1>(a, backward, stream);
+    if (vec == 8) return launch<uint16_t, 8>(a, backward, stream);
+    return vec == 2 ? launch<uint16_t, 2>(a, backward, stream) : launch<uint16_t, 1>(a, backward, stream);
+}
+
+// every grid's extent in threads fits 32 bits
+bool grid_ok(const Args &a, long long chunks) {
+    return chunks * a.groups <= 0xffffffffLL / 64 - kThreads && chunks <= 0x7fffffffLL;
+}
+
+}  // namespace
+}  // namespace gnorm
+
+using namespace gnorm;
+
+extern "C" {
+
+size_t group_norm_backward_workspace(const group_norm_problem *in) {
+    Checked c;
+    if (check_problem(in, c) != RWKV7_OK) return 0;
+    return (size_t)chunks_of(c.a, backward_rows(c.a)) * 2 * c.a.groups * c.a.size * 4;
+}
+
+rwkv7_status group_norm_forward(const group_norm_problem *in, const void *x, const void *gate,
+                                const float *weight, const float *bias, void *y, void *stream) {
+    Checked c;
+    const rwkv7_status st = check_problem(in, c);
+    if (st != RWKV7_OK) return st;
+    Args &a = c.a;
+    if (a.rows > 0 && (!x || !y)) return RWKV7_ERR_NULL;
+    const size_t esz = (size_t)c.esz;
+    if (!aligned(x, esz) || !aligned(gate, esz) || !aligned(y, esz) || !aligned(weight, 4) || !aligned(bias, 4))
+        return RWKV7_ERR_ALIGN;
+    if (!grid_ok(a, a.rows)) return RWKV7_ERR_SHAPE;
+    const long long C = (long long)a.groups * a.size;
+    const size_t params = (size_t)C * 4;
+    const bool in_place = y == x && a.x_stride == C;
+    if (!disjoint({{y, extent(a.rows, C, C, c.esz)}},
+                  {{in_place ? nullptr : x, extent(a.rows, a.x_stride, C, c.esz)},
+                   {gate, extent(a.rows, a.gate_stride, C, c.esz)}, {weight, params}, {bias, params}}))
+        return RWKV7_ERR_ALIAS;
+    a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.y = y;
+    return launch(a, c.esz, piece(a, c.esz, {x, gate, y}), false,
+                  static_cast<hipStream_t>(stream)) == hipSuccess
+               ? RWKV7_OK
+               : RWKV7_ERR_HIP;
+}
+
+rwkv7_status group_norm_backward(const group_norm_problem *in, const void *x, const void *gate,
+                                 const float *weight, const float *bias, const void *dy, void *dx,
+                                 void *dgate, float *dweight, float *dbias, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    Checked c;
+    const rwkv7_status st = check_problem(in, c);
+    if (st != RWKV7_OK) return st;
+    Args &a = c.a;
+    if (a.rows > 0 && (!x || !dy || !dx)) return RWKV7_ERR_NULL;
+    if (a.rows > 0 && !gate != !dgate) return RWKV7_ERR_NULL;
+    const size_t esz = (size_t)c.esz;
+    for (const void *p : {x, gate, dy, (const void *)dx, (const void *)dgate})
+        if (!aligned(p, esz)) return RWKV7_ERR_ALIGN;
+    for (const float *p : {weight, bias, (const float *)dweight, (const float *)dbias})
+        if (!aligned(p, 4)) return RWKV7_ERR_ALIGN;
+    const int per_team = backward_rows(a);
+    const long long chunks = chunks_of(a, per_team), C = (long long)a.groups * a.size;
+    if (!grid_ok(a, chunks)) return RWKV7_ERR_SHAPE;
+    const bool sums = dweight || dbias;
+    const size_t need = sums ? (size_t)chunks * 2 * C * 4 : 0;
+    if (need && (!workspace || workspace_bytes < need)) return RWKV7_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return RWKV7_ERR_ALIGN;
+    const size_t params = (size_t)C * 4, dense = extent(a.rows, C, C, c.esz);
+    if (!disjoint({{dx, dense}, {dgate, dense}, {dweight, params}, {dbias, params}, {workspace, need}},
+                  {{x, extent(a.rows, a.x_stride, C, c.esz)}, {gate, extent(a.rows, a.gate_stride, C, c.esz)},
+                   {weight, params}, {bias, params}, {dx == dy ? nullptr : dy, dense}}))
+        return RWKV7_ERR_ALIAS;
+    a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.dy = dy;
+    a.dx = dx; a.dgate = dgate;
+    a.sums = sums ? static_cast<float *>(workspace) : nullptr;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (launch(a, c.esz, piece(a, c.esz, {x, gate, dy, dx, dgate}), true, s) != hipSuccess)
+        return RWKV7_ERR_HIP;
+    if (sums) {
+        hipLaunchKernelGGL(sum_kernel, dim3((unsigned)((2 * C + 63) / 64)), dim3(1024), 0, s,
+                           static_cast<const float *>(workspace), dweight, dbias, (int)chunks, (int)C);
+        if (hipGetLastError() != hipSuccess) return RWKV7_ERR_HIP;
+    }
+    return RWKV7_OK;
+}
+
+}  // extern "C"
