@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "group_norm.h"
 #include "wkv7_device.h"
@@ -77,20 +78,24 @@ __device__ __forceinline__ float sigmoid(float x) {
         return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
     return 1.f / (1.f + expf(-x));
 }
+// silu and sigmoid, and with them their derivatives; `silu` is the same for all lanes
 template <class E>
-__device__ __forceinline__ float activate(float x, int act) {
-    if (act == GROUP_NORM_NONE) return x;
-    const float s = sigmoid<E>(x);
-    return act == GROUP_NORM_SILU ? x * s : s;
+__device__ __forceinline__ float activate(float x, bool silu) {
+    return sigmoid<E>(x) * (silu ? x : 1.f);
 }
-// the activation, and its derivative
 template <class E>
-__device__ __forceinline__ float activate(float x, int act, float &slope) {
-    slope = 1.f;
-    if (act == GROUP_NORM_NONE) return x;
-    const float s = sigmoid<E>(x);
-    slope = act == GROUP_NORM_SILU ? s + x * (s - s * s) : s - s * s;
-    return act == GROUP_NORM_SILU ? x * s : s;
+__device__ __forceinline__ float activate(float x, bool silu, float &slope) {
+    const float s = sigmoid<E>(x), d = s - s * s;
+    slope = silu ? s + x * d : d;
+    return s * (silu ? x : 1.f);
+}
+// calls f with whether there is no activation, known to the compiler
+template <class F>
+__device__ __forceinline__ void by_kind(int act, F f) {
+    if (act == GROUP_NORM_NONE)
+        f(std::integral_constant<bool, true>());
+    else
+        f(std::integral_constant<bool, false>());
 }
 
 // Which group, and which rows, a thread's team has; the lane's number in the team.
@@ -108,7 +113,7 @@ struct Place {
 };
 
 // the statistics of R rows at once, one chain of sums beside the other: afterwards x holds u
-template <int L, int N, int R>
+template <int L, int N, int R, bool FULL>
 __device__ __forceinline__ void normalize(float (&x)[R][N], float (&rstd)[R], const bool (&has)[N],
                                           const Args &a) {
     float mean[R], var[R];
@@ -125,19 +130,19 @@ __device__ __forceinline__ void normalize(float (&x)[R][N], float (&rstd)[R], co
         var[r] = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[r][i] = has[i] ? x[r][i] - mean[r] : 0.f;
+            x[r][i] = FULL || has[i] ? x[r][i] - mean[r] : 0.f;
             var[r] += x[r][i] * x[r][i];
         }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        rstd[r] = 1.f / sqrtf(team_sum<L>(var[r]) * a.inv_size + a.eps);
+        rstd[r] = rsqrtf(team_sum<L>(var[r]) * a.inv_size + a.eps);
 #pragma unroll
         for (int i = 0; i < N; ++i) x[r][i] *= rstd[r];
     }
 }
 
-template <class E, int VEC, int L, int NV, int R, bool GATE>
+template <class E, int VEC, int L, int NV, int R, bool GATE, bool FULL>
 __global__ __launch_bounds__(kThreads) void forward_kernel(Args a) {
     constexpr int N = VEC * NV;
     using V = Raw<E, VEC>;
@@ -149,9 +154,9 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Args a) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int piece = v * L + at.lane;
-        col[v] = at.group * a.size + (piece < pieces ? piece : 0) * VEC;
+        col[v] = at.group * a.size + (FULL || piece < pieces ? piece : 0) * VEC;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = piece < pieces;
+        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = FULL || piece < pieces;
     }
     const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate);
     const long long C = (long long)a.groups * a.size;
@@ -175,35 +180,37 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(Args a) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < N; ++i) u[r][i] = has[i] ? widen(rx[r][i / VEC].e[i % VEC]) : 0.f;
-    normalize<L, N, R>(u, rstd, has, a);
+        for (int i = 0; i < N; ++i) u[r][i] = FULL || has[i] ? widen(rx[r][i / VEC].e[i % VEC]) : 0.f;
+    normalize<L, N, R, FULL>(u, rstd, has, a);
+    const bool silu = a.act == GROUP_NORM_SILU;
+    by_kind(a.act, [&](auto none) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (at.first + r >= at.end) break;
-        E *yp = static_cast<E *>(a.y) + (at.first + r) * C;
+        for (int r = 0; r < R; ++r) {
+            if (at.first + r >= at.end) break;
+            E *yp = static_cast<E *>(a.y) + (at.first + r) * C;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float y[VEC];
+            for (int v = 0; v < NV; ++v) {
+                float y[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int k = v * VEC + i;
-                const float n = u[r][k] * w[k] + b[k];
-                if constexpr (GATE)
-                    y[i] = n * activate<E>(widen(rg[r][v].e[i]), a.act);
-                else
-                    y[i] = activate<E>(n, a.act);
-            }
-            if (has[v * VEC]) {
-                V out;
-                narrow(out, y);
-                *reinterpret_cast<V *>(yp + col[v]) = out;
+                for (int i = 0; i < VEC; ++i) {
+                    const int k = v * VEC + i;
+                    const float n = u[r][k] * w[k] + b[k];
+                    const float z = GATE ? widen(rg[r][v].e[i]) : n;
+                    const float act = none ? z : activate<E>(z, silu);
+                    y[i] = GATE ? n * act : act;
+                }
+                if (has[v * VEC]) {
+                    V out;
+                    narrow(out, y);
+                    *reinterpret_cast<V *>(yp + col[v]) = out;
+                }
             }
         }
-    }
+    });
 }
 
-template <class E, int VEC, int L, int NV, bool GATE>
-__global__ __launch_bounds__(kThreads) void backward_kernel(Args a) {
+template <class E, int VEC, int L, int NV, bool GATE, bool FULL>
+__global__ __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) void backward_kernel(Args a) {
     constexpr int N = VEC * NV;
     using V = Raw<E, VEC>;
     const Place<L> at(a);
@@ -214,9 +221,9 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Args a) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int piece = v * L + at.lane;
-        col[v] = at.group * a.size + (piece < pieces ? piece : 0) * VEC;
+        col[v] = at.group * a.size + (FULL || piece < pieces ? piece : 0) * VEC;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = piece < pieces;
+        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = FULL || piece < pieces;
     }
     const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate),
             *dp = static_cast<const E *>(a.dy);
@@ -238,36 +245,34 @@ __global__ __launch_bounds__(kThreads) void backward_kernel(Args a) {
             if constexpr (GATE) rg[v] = *reinterpret_cast<const V *>(gp + row * a.gate_stride + col[v]);
         }
     };
+    const bool silu = a.act == GROUP_NORM_SILU;
     fetch(at.first);
     for (long long row = at.first; row < at.end; ++row) {
         float u[1][N], rstd[1], gate[N], dy[N], dn[N], dz[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            u[0][i] = has[i] ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
-            dy[i] = has[i] ? widen(rd[i / VEC].e[i % VEC]) : 0.f;
+            u[0][i] = FULL || has[i] ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
+            dy[i] = FULL || has[i] ? widen(rd[i / VEC].e[i % VEC]) : 0.f;
             if constexpr (GATE) gate[i] = widen(rg[i / VEC].e[i % VEC]);
         }
         if (row + 1 < at.end) fetch(row + 1);  // (dx may be dy: not this row's again)
-        normalize<L, N, 1>(u, rstd, has, a);
+        normalize<L, N, 1, FULL>(u, rstd, has, a);
         float sum = 0.f, along = 0.f;
+        by_kind(a.act, [&](auto none) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float n = u[0][i] * w[i] + b[i];
-            float slope;
-            if constexpr (GATE) {
-                const float act = activate<E>(gate[i], a.act, slope);
-                dn[i] = dy[i] * act;
-                dz[i] = dy[i] * n * slope;
-            } else {
-                activate<E>(n, a.act, slope);
-                dn[i] = dy[i] * slope;
+            for (int i = 0; i < N; ++i) {
+                const float n = u[0][i] * w[i] + b[i];
+                float slope = 1.f, act = GATE ? gate[i] : n;
+                if constexpr (!none) act = activate<E>(act, silu, slope);
+                dn[i] = dy[i] * (GATE ? act : slope);
+                if constexpr (GATE) dz[i] = dy[i] * n * slope;
+                dw[i] += dn[i] * u[0][i];
+                db[i] += dn[i];
+                dn[i] = FULL || has[i] ? dn[i] * w[i] : 0.f;
+                sum += dn[i];
+                along += dn[i] * u[0][i];
             }
-            dw[i] += dn[i] * u[0][i];
-            db[i] += dn[i];
-            dn[i] = has[i] ? dn[i] * w[i] : 0.f;
-            sum += dn[i];
-            along += dn[i] * u[0][i];
-        }
+        });
         sum = a.rms ? 0.f : team_sum<L>(sum) * a.inv_size;
         along = team_sum<L>(along) * a.inv_size;
 #pragma unroll
@@ -326,6 +331,10 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float *sums, float *dwe
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+// rows that the forward's teams have at once
+template <int NV>
+constexpr int kRows = NV == 1 ? 4 : NV == 2 ? 2 : 1;
+
 struct Shape {
     int L, nv;  // lanes of a team, 8 to 64, and pieces of a lane, both powers of two
 };
@@ -408,18 +417,25 @@ int piece(const Args &a, int esz, std::initializer_list<const void *> ps) {
     return fits(16 / esz) ? 16 / esz : esz == 2 && fits(2) ? 2 : 1;
 }
 
+template <class E, int VEC, int L, int NV, bool FULL>
+void (*kernel_of(const Args &a, bool backward, bool many))(Args) {
+    constexpr int R = kRows<NV>;
+    if (backward)
+        return a.gate ? &backward_kernel<E, VEC, L, NV, true, FULL> : &backward_kernel<E, VEC, L, NV, false, FULL>;
+    if (many)
+        return a.gate ? &forward_kernel<E, VEC, L, NV, R, true, FULL> : &forward_kernel<E, VEC, L, NV, R, false, FULL>;
+    return a.gate ? &forward_kernel<E, VEC, L, NV, 1, true, FULL> : &forward_kernel<E, VEC, L, NV, 1, false, FULL>;
+}
 template <class E, int VEC, int L, int NV>
 hipError_t launch(Args a, bool backward, hipStream_t stream) {
     // several rows of a team at once where there are teams enough without
-    constexpr int R = NV == 1 ? 4 : NV == 2 ? 2 : 1;
+    constexpr int R = kRows<NV>;
     const bool many = R > 1 && a.rows * a.groups * L >= 64LL * 8192;
-    void (*kernel)(Args);
-    if (backward)
-        kernel = a.gate ? &backward_kernel<E, VEC, L, NV, true> : &backward_kernel<E, VEC, L, NV, false>;
-    else if (many)
-        kernel = a.gate ? &forward_kernel<E, VEC, L, NV, R, true> : &forward_kernel<E, VEC, L, NV, R, false>;
-    else
-        kernel = a.gate ? &forward_kernel<E, VEC, L, NV, 1, true> : &forward_kernel<E, VEC, L, NV, 1, false>;
+    // teams without idle lanes (the usual sizes) need no masks
+    void (*kernel)(Args) = nullptr;
+    if constexpr (VEC * sizeof(E) == 16)
+        if (a.size == VEC * L * NV) kernel = kernel_of<E, VEC, L, NV, true>(a, backward, many);
+    if (!kernel) kernel = kernel_of<E, VEC, L, NV, false>(a, backward, many);
     a.per_team = backward ? backward_rows(a) : many ? R : 1;
     const long long teams = chunks_of(a, a.per_team) * a.groups;
     hipLaunchKernelGGL(kernel, dim3((unsigned)((teams * L + kThreads - 1) / kThreads)), dim3(kThreads), 0,

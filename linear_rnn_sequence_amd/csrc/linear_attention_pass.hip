@@ -22,7 +22,7 @@
 // reads it out as it does S, and at the end takes its product with the cotangent.  (The usual
 // sum of position times q dq - k dk cancels to nothing for long sequences.)
 //
-// Layout: a wave owns 16 rows of the state over all KD columns, as matrix-core result
+// Layout: a wave owns 16 or 32 rows of the state over all KD columns, as matrix-core result
 // tiles [columns, rows]: S x^T and the products with z^T need nothing of another wave.  The
 // chunk's rows of x, y and z lie in shared memory; x y^T, six fragments of the lower
 // triangle, is computed by the waves together and passed through it.
@@ -75,6 +75,7 @@ template <class E, int N>
 struct Parts {
     Frag<E> p[sizeof(E) == 2 ? N : 1];
     static constexpr int kN = sizeof(E) == 2 ? N : 1;
+    Parts() = default;
     __device__ __forceinline__ Parts(f32x4 a, f32x4 b) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
@@ -89,13 +90,69 @@ struct Parts {
     }
 };
 
-// Rows of a chunk on their way from memory to a tile in shared memory; in a reversed pass row
-// r is the live - 1 - r-th in memory.  Rows behind `live` are zeros.
+// A chunk's 64 rows of C channels in shared memory.  The rows are a few pieces of 16 bytes
+// longer than their channels, such that reads along 16 rows and down the columns of 16 meet
+// different banks (mostly: 16 bits and 12 words more, a transposing read takes 3 cycles for 2),
+// and so that every address is a lane's own plus a number known to the compiler, where a
+// swizzle has to be computed for each (a third of the kernel's vector instructions).
+//
+// Contraction over tokens: element j of lane group g is the token 32 st + 4 g + j, for j >= 4
+// 32 st + 16 + 4 g + j - 4, which is how two result tiles of 16 tokens make up an operand.
+template <class E, int C>
+struct Plane {
+    static constexpr int kWords = C * (int)sizeof(E) / 4 + (sizeof(E) == 4 ? 4 : 12), kRow = 4 * kWords;
+    static constexpr int kBytes = kChunk * kRow;
+    char *p;
+    // a lane's place for reads along the rows: row lo, channels 8 g ..
+    static __device__ __forceinline__ int along(int g, int lo) { return lo * kRow + 8 * g * (int)sizeof(E); }
+    // channels 32 ks + 8 g .. of row 16 i + lo; `at`: p + along()
+    static __device__ __forceinline__ Frag<E> rows(const char *at, int i, int ks) {
+        at += 16 * i * kRow + 32 * ks * (int)sizeof(E);
+        Frag<E> f;
+        if constexpr (sizeof(E) == 2) {
+            f.v = *reinterpret_cast<const u32x4 *>(at);
+        } else {
+            f.v[0] = *reinterpret_cast<const f32x4 *>(at);
+            f.v[1] = *reinterpret_cast<const f32x4 *>(at + 16);
+        }
+        return f;
+    }
+    // A lane's place for reads down the columns c(lo) = 8 (lo >> 2) + (lo & 3) (STEP 8) or lo
+    // (STEP 4).  In bf16 by transposing reads: ds_read_b64_tr_b16 takes from each lane of a
+    // group of 16 the address of four elements (lane i: row i >> 2, columns STEP (i & 3) ..)
+    // and returns to lane l the four rows' elements of column l.
+    template <int STEP>
+    static __device__ __forceinline__ int down(int g, int lo) {
+        if constexpr (sizeof(E) == 2) return (4 * g + (lo >> 2)) * kRow + STEP * (lo & 3) * 2;
+        return 4 * g * kRow + (STEP * (lo >> 2) + (lo & 3)) * 4;
+    }
+    // the 32 tokens of st of column col + c(lo); `at`: p + down()
+    static __device__ __forceinline__ Frag<E> cols(const char *at, int st, int col) {
+        at += 32 * st * kRow + col * (int)sizeof(E);
+        Frag<E> f;
+        if constexpr (sizeof(E) == 2) {
+            typedef short s4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s4 lds_s4;
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at)),
+                        b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                          (lds_s4 *)(at + 16 * kRow)));
+            f.v = u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f.v[j >> 2][j & 3] = *reinterpret_cast<const float *>(at + (j < 4 ? j : 12 + j) * kRow);
+        }
+        return f;
+    }
+};
+
+// Rows of a chunk on their way from memory to a plane; in a reversed pass row r is the
+// live - 1 - r-th in memory.  Rows behind `live` are zeros.
 template <class E, int C, int THREADS>
 struct Rows {
-    static constexpr int kRowPieces = Tile<E, C>::kRowPieces, kPiece = Tile<E, C>::kPiece;
-    static constexpr int kPer = kChunk * kRowPieces / THREADS;
-    static_assert(kChunk * kRowPieces % THREADS == 0, "whole pieces per thread");
+    static constexpr int kPiece = 16 / (int)sizeof(E), kRowPieces = C / kPiece;  // elements, per row
+    static constexpr int kPer = kChunk * kRowPieces / THREADS, kStep = THREADS / kRowPieces;
+    static_assert(THREADS % kRowPieces == 0 && kPer * kStep == kChunk, "a thread's pieces are kStep rows apart");
     u32x4 d[kPer];
     static __device__ __forceinline__ unsigned offset(int row, int col, int stride, int live,
                                                       bool reverse) {
@@ -103,40 +160,43 @@ struct Rows {
         const unsigned at = reverse ? (unsigned)(live - 1 - row) : (unsigned)row;
         return (at * (unsigned)stride + (unsigned)col) * (unsigned)sizeof(E);
     }
+    static __device__ __forceinline__ unsigned first(int stride, int live, bool reverse, int tid) {
+        return offset(tid / kRowPieces, tid % kRowPieces * kPiece, stride, live, reverse);
+    }
+    static __device__ __forceinline__ unsigned step(int stride, bool reverse) {
+        const unsigned s = (unsigned)(kStep * (int)sizeof(E)) * (unsigned)stride;
+        return reverse ? 0u - s : s;
+    }
+    static __device__ __forceinline__ int place(int tid) {
+        return tid / kRowPieces * Plane<E, C>::kRow + tid % kRowPieces * 16;
+    }
     __device__ __forceinline__ void load(const E *src, int stride, int live, bool reverse, int tid) {
         const Buffer b(src, row_bytes<E>(live, stride));
+        const unsigned from = first(stride, live, reverse, tid), next = step(stride, reverse);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int piece = tid + i * THREADS;
-            d[i] = b.load16(offset(piece / kRowPieces, piece % kRowPieces * kPiece, stride, live,
-                                   reverse));
-        }
+        for (int i = 0; i < kPer; ++i) d[i] = b.load16(from + i * next);
     }
-    __device__ __forceinline__ void put(Tile<E, C> t, int tid) const {
+    __device__ __forceinline__ void put(char *plane, int tid) const {
+        char *at = plane + place(tid);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int piece = tid + i * THREADS;
-            *reinterpret_cast<u32x4 *>(
-                t.p + t.offset(piece / kRowPieces, piece % kRowPieces * kPiece)) = d[i];
-        }
+        for (int i = 0; i < kPer; ++i)
+            *reinterpret_cast<u32x4 *>(at + i * kStep * Plane<E, C>::kRow) = d[i];
     }
     // the way back, from the pieces that put() will write next
-    static __device__ __forceinline__ void store(Tile<E, C> t, E *dst, int stride, int live,
+    static __device__ __forceinline__ void store(const char *plane, E *dst, int stride, int live,
                                                  bool reverse, int tid) {
         const Buffer b(dst, row_bytes<E>(live, stride));
+        const unsigned from = first(stride, live, reverse, tid), next = step(stride, reverse);
+        const char *at = plane + place(tid);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int piece = tid + i * THREADS;
-            const int row = piece / kRowPieces, col = piece % kRowPieces * kPiece;
-            b.store16(offset(row, col, stride, live, reverse),
-                      *reinterpret_cast<const u32x4 *>(t.p + t.offset(row, col)));
-        }
+        for (int i = 0; i < kPer; ++i)
+            b.store16(from + i * next,
+                      *reinterpret_cast<const u32x4 *>(at + i * kStep * Plane<E, C>::kRow));
     }
 };
 
 // The head's log decay to the base 2 (below -200 it is 0 in float32, -infinity with it; a NaN
-// stays one) and its powers.  The exponent keeps more than a float's bits: what is off by 2^-24
-// of a chunk's exponent would be off by 512 of these after 512 chunks.
+// stays one) and its powers, of which the exponents keep more than a float's bits.
 struct Decay {
     double g2;
     __device__ __forceinline__ explicit Decay(float g)
@@ -146,41 +206,40 @@ struct Decay {
         const float hi = (float)x;
         return exp2f(hi) * (1.f + 0.6931472f * (float)(x - hi));
     }
-    // as the sum of two floats: a chunk's, which is applied once per chunk
-    __device__ __forceinline__ Sum2 exact(int n) const {
-        const double x = exp2(g2 * n);
-        const float hi = (float)x;
-        return Sum2{hi, (float)(x - hi)};
-    }
+    __device__ __forceinline__ double exact(int n) const { return exp2(g2 * n); }
 };
 
 template <class E, int KD, int VD, Mode MODE>
 struct Shared {
-    static constexpr int kTileK = tile_bytes<E, KD>(kChunk), kTileV = tile_bytes<E, VD>(kChunk);
+    // Waves of a workgroup, and tiles of 16 rows of the state that each owns.
+    static constexpr int kOwn = sizeof(E) == 2 && MODE != kGrad && VD >= KD ? 2 : 1, kWaves = VD / 16 / kOwn;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kTileK = Plane<E, KD>::kBytes, kTileV = Plane<E, VD>::kBytes;
     static constexpr int kFrag = 2048;  // bf16: two parts, float: two halves
     static constexpr int kY = 0, kZ = kTileK, kX = kZ + kTileV;
     static constexpr int kP = kX + (MODE == kSum ? 0 : kTileK);
     static constexpr int kE = kP + (MODE == kSum ? 0 : 6 * kFrag);
-    static constexpr int kPowers = kE + (MODE == kGrad ? kTileV : 0);
-    static constexpr int kBytes = kPowers + 68 * 4;
+    // weights: of the tokens in the state [64], of pairs of tokens by their distance
+    // (-64 .. 63; 0 below 0)
+    static constexpr int kWrite = kE + (MODE == kGrad ? kTileV : 0), kPair = kWrite + kChunk * 4;
+    static constexpr int kBytes = kPair + 2 * kChunk * 4;
     // the next chunk's rows are on their way while this one is computed (in float they
     // would take the registers that its products need)
     static constexpr bool kAhead = sizeof(E) == 2 && !(MODE == kGrad && KD > VD);
-    // kernels that would need more registers than there are
-    static constexpr bool kTight = sizeof(E) == 4 || MODE == kGrad;
     // tiles of columns that the state's products have in registers at a time
-    static constexpr int kGroup = sizeof(E) == 4 && MODE == kGrad ? 1 : kTight ? 2 : 4;
+    static constexpr int kGroup = sizeof(E) == 4 || MODE == kGrad ? 2 : 4;
 };
 
 template <class E, class O, int KD, int VD, Mode MODE>
-__global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(PassArgs a) {
+__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4 ? 1 : 2) void pass_kernel(
+    PassArgs a) {
     using L = Shared<E, KD, VD, MODE>;
-    constexpr int W = VD / 16, kThreads = 64 * W, KS = KD / 32, M = KD / 16;
-    constexpr int kTiles = 12 / W + (12 % W ? 1 : 0);  // of x y^T per wave
+    constexpr int W = L::kWaves, NT = L::kOwn, kThreads = L::kThreads, KS = KD / 32, M = KD / 16;
+    constexpr int kTiles = (10 + W - 1) / W;  // of x y^T per wave
     extern __shared__ __align__(16) char lds[];
     const Pass &p = a.pass[blockIdx.y];
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int lane = tid & 63, g = lane >> 4, lo = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63,
+              wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
     const int unit = (int)(blockIdx.x / a.heads), h = (int)(blockIdx.x % a.heads);
     const bool reverse = p.shift == 0;
 
@@ -206,23 +265,33 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
     const size_t state_size = (size_t)VD * KD;
 
     const Decay decay(a.g[h / a.parts]);
-    float *pw = reinterpret_cast<float *>(lds + L::kPowers);
-    if (tid <= kChunk) pw[tid] = decay.power(tid);
+    float *write = reinterpret_cast<float *>(lds + L::kWrite), *pairs = reinterpret_cast<float *>(lds + L::kPair);
+    if (tid < kChunk) {
+        write[tid] = p.write * decay.power(kChunk - p.shift - tid);
+        pairs[tid] = 0.f;
+        pairs[kChunk + tid] = p.intra * decay.power(tid);
+    }
 
-    // the wave's rows of a state in memory: row own0 + lo, columns tile_row(m, 4g) ..
-    const int own0 = 16 * wave;
-    auto load_state = [&](f32x4(&S)[M], const float *base) {
+    // the wave's rows of a state in memory: row own0 + 16 n + lo, columns tile_row(m, 4g) ..
+    const int own0 = 16 * NT * wave;
+    auto load_state = [&](f32x4(&S)[NT][M], const float *base) {
+        if (p.turned) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const int row = own0 + lo, col = tile_row(m, 4 * g);
-            if (p.turned)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[m][e] = base[(col + e) * VD + row];
-            else
-                S[m] = *reinterpret_cast<const f32x4 *>(base + row * KD + col);
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[n][m][e] = base[(tile_row(m, 4 * g) + e) * VD + own0 + 16 * n + lo];
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    S[n][m] = *reinterpret_cast<const f32x4 *>(base + (own0 + 16 * n + lo) * KD + tile_row(m, 4 * g));
         }
     };
-    f32x4 S[M], R[MODE == kGrad ? M : 1];
+    f32x4 S[NT][M], R[MODE == kGrad ? M : 1];
     const float *from = nullptr;
     if (MODE != kSum && a.seg) {
         from = p.unit_states + ((size_t)unit * a.heads + h) * state_size;
@@ -234,7 +303,9 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
         load_state(S, from);
     } else {
 #pragma unroll
-        for (int m = 0; m < M; ++m) S[m] = zero();
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < M; ++m) S[n][m] = zero();
     }
     if constexpr (MODE == kGrad)
 #pragma unroll
@@ -248,9 +319,16 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
     const int row = a.heads * VD;
     O *op = static_cast<O *>(p.out) + token * row + h * VD;
 
-    const Tile<E, KD> tx{reinterpret_cast<E *>(lds + L::kX)}, ty{reinterpret_cast<E *>(lds + L::kY)};
-    const Tile<E, VD> tz{reinterpret_cast<E *>(lds + L::kZ)}, te{reinterpret_cast<E *>(lds + L::kE)};
-    char *frags = lds + L::kP;
+    using PK = Plane<E, KD>;
+    using PV = Plane<E, VD>;
+    char *const px = lds + L::kX, *const py = lds + L::kY, *const pz = lds + L::kZ, *const pe = lds + L::kE;
+    const char *const x_rows = px + PK::along(g, lo), *const y_rows = py + PK::along(g, lo),
+               *const y_cols = py + PK::template down<8>(g, lo),
+               *const z_cols = pz + PV::template down<4>(g, lo) + own0 * (int)sizeof(E),
+               *const z_rows = pz + PV::along(g, lo), *const e_rows = pe + PV::along(g, lo);
+    // channels own0 + 4 g .. of row lo
+    const int own_place = lo * PV::kRow + (own0 + 4 * g) * (int)sizeof(E);
+    char *const frags = lds + L::kP + lane * 16;
 
     auto live_of = [&](int c) {
         const int left = len - c * kChunk;
@@ -272,207 +350,279 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
         if constexpr (MODE == kGrad) ge.load(ep + at * p.e_stride, p.e_stride, live, reverse, tid);
     };
     auto put = [&]() {
-        if (MODE != kSum) gx.put(tx, tid);
-        gy.put(ty, tid);
-        gz.put(tz, tid);
-        if constexpr (MODE == kGrad) ge.put(te, tid);
+        if (MODE != kSum) gx.put(px, tid);
+        gy.put(py, tid);
+        gz.put(pz, tid);
+        if constexpr (MODE == kGrad) ge.put(pe, tid);
     };
     if (chunks > 0) {
         fetch(0);
         put();
     }
+    // Fragments 0, 1, 2 .. of x y^T: token tiles 0 and 1 with the tokens 0 .. 31, 2 and 3 with
+    // both halves.  Tiles (0, 1) and (2, 3) lie above the diagonal and stay zero.
+    if (MODE != kSum && wave == 0)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int f = 0; f <= 3; f += 3) {
+                if constexpr (sizeof(E) == 2)
+                    *reinterpret_cast<u32x2 *>(frags + f * L::kFrag + 1024 * half + 8) = u32x2{0u, 0u};
+                else if (half)
+                    *reinterpret_cast<f32x4 *>(frags + f * L::kFrag + 1024) = zero();
+            }
     __syncthreads();
 
-    // powers that every whole chunk uses: of the readout of token tile_row(i, lo), of the wave's
-    // tiles of x y^T, and of the tokens 32 st + 8 g + j in the state
-    float rd[4], pair[kTiles][4], kd[2][8];
+    float rd[4];  // weights of the readout of the tokens 16 i + lo
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rd[i] = p.read * pw[tile_row(i, lo) + p.shift];
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-        const int t = wave + x * W, f = t < 12 ? t >> 1 : 0, i = tile_row(kLowTile[f], lo);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = tile_row(2 * kLowStep[f] + (t & 1), 4 * g + e);
-            pair[x][e] = j <= i ? p.intra * pw[i - j] : 0.f;
-        }
-    }
-    auto weights = [&](int live) {
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int n = live - p.shift - (32 * st + 8 * g + j);
-                kd[st][j] = n < 0 ? 0.f : p.write * pw[n];
-            }
-    };
-    weights(kChunk);
-    Sum2 whole = decay.exact(kChunk);
+    for (int i = 0; i < 4; ++i) rd[i] = p.read * decay.power(16 * i + lo + p.shift);
+    // The state's decay over a chunk, as a float: what that is off by goes into the next one,
+    // so that after any number of chunks the state has been decayed by the exact power.
+    double whole = decay.exact(kChunk), owed = 1.0;
+    const double rest_of = decay.exact(live_of(chunks - 1));  // over the last chunk
+    const double back = whole > 1e-30 ? 1.0 / whole : 0.0;
     double dg = 0.0;
 
     for (int c = 0; c < chunks; ++c) {
         const int live = live_of(c);
         if (L::kAhead) fetch(c + 1);
-        if constexpr (L::kTight) {  // addresses in shared memory are formed again in every chunk
-            asm volatile("" : "+v"(lane));
-            g = lane >> 4;
-            lo = lane & 15;
+        if (live < kChunk) {  // the last one (its other weights are read behind the next barrier)
+            whole = rest_of;
+            if (tid < kChunk) {
+                const int n = live - p.shift - tid;
+                write[tid] = n < 0 ? 0.f : p.write * decay.power(n);
+            }
+            if (MODE == kSum) __syncthreads();
         }
-        if (live < kChunk) {
-            weights(live);
-            whole = decay.exact(live);
-        }
-        f32x4 out[4];
+        const double want = whole * owed;
+        const float fade = (float)want;
+        owed = 1.0 + (want - fade) * back;
+        f32x4 out[NT][4];
         float dg_chunk = 0.f;
         if constexpr (MODE != kSum) {
-            // x y^T, masked and decayed
+            // x y^T, masked and decayed: tiles (it, jt) of the lower triangle, row by row; the waves
+            // take turns (and those without a tile left do the last one again)
+            f32x4 d[kTiles], b[MODE == kGrad ? kTiles : 1];
+            int it[kTiles], jt[kTiles];
 #pragma unroll
-            for (int x = 0; x < kTiles; ++x) {
-                const int t = wave + x * W;
-                if (t < 12) {
-                    const int f = t >> 1, jt = 2 * kLowStep[f] + (t & 1), it = kLowTile[f];
-                    f32x4 d = zero();
+            for (int n = 0; n < kTiles; ++n) {
+                const int t = wave + n * W < 10 ? wave + n * W : 9;
+                it[n] = 0xffa94 >> 2 * t & 3;
+                jt[n] = 0xe4910 >> 2 * t & 3;
+                d[n] = zero();
+                if constexpr (MODE == kGrad) b[n] = zero();
+            }
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        d = mma(ty.rows(tile_row(jt, lo), 32 * ks, g), tx.rows(tile_row(it, lo), 32 * ks, g), d);
-                    const int i = tile_row(it, lo), j0 = tile_row(jt, 4 * g);
-                    f32x4 w;
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = j0 + e <= i ? pair[x][e] * d[e] : 0.f;
+                for (int n = 0; n < kTiles; ++n)
+                    d[n] = mma(PK::rows(y_rows, jt[n], ks), PK::rows(x_rows, it[n], ks), d[n]);
+            if constexpr (MODE == kGrad) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < VD / 32; ++ks)
+#pragma unroll
+                    for (int n = 0; n < kTiles; ++n)
+                        b[n] = mma(PV::rows(z_rows, jt[n], ks), PV::rows(e_rows, it[n], ks), b[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+                const int far = 16 * (it[n] - jt[n]) + lo - 4 * g;  // i - j of element 0
+                const float *weight = pairs + kChunk + far;
+                f32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = weight[-e] * d[n][e];
+                    w[e] = far >= e ? w[e] : 0.f;  // (also where d is not finite)
                     if constexpr (MODE == kGrad) {
-                        f32x4 b = zero();
-#pragma unroll
-                        for (int ks = 0; ks < VD / 32; ++ks)
-                            b = mma(tz.rows(tile_row(jt, lo), 32 * ks, g), te.rows(tile_row(it, lo), 32 * ks, g), b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j0 + e < i) dg_chunk += (float)(i - j0 - e) * w[e] * b[e];
+                        const float one = (float)(far - e) * w[e] * b[n][e];
+                        dg_chunk += far > e && wave + n * W < 10 ? one : 0.f;
                     }
-                    char *at = frags + f * L::kFrag;
-                    if constexpr (sizeof(E) == 2) {
-                        const u32x2 hi = {cvt_pk(w[0], w[1]), cvt_pk(w[2], w[3])};
-                        *reinterpret_cast<u32x2 *>(at + lane * 16 + 8 * (t & 1)) = hi;
-                        w -= f32x4{wkv7::bf16_lo(hi[0]), wkv7::bf16_hi(hi[0]), wkv7::bf16_lo(hi[1]),
-                                   wkv7::bf16_hi(hi[1])};
-                        *reinterpret_cast<u32x2 *>(at + 1024 + lane * 16 + 8 * (t & 1)) =
-                            u32x2{cvt_pk(w[0], w[1]), cvt_pk(w[2], w[3])};
-                    } else {
-                        *reinterpret_cast<f32x4 *>(at + lane * 16 + 1024 * (t & 1)) = w;
-                    }
+                }
+                char *at = frags + (it[n] + (it[n] == 3) + (jt[n] >> 1)) * L::kFrag;
+                if constexpr (sizeof(E) == 2) {
+                    const u32x2 hi = {cvt_pk(w[0], w[1]), cvt_pk(w[2], w[3])};
+                    *reinterpret_cast<u32x2 *>(at + 8 * (jt[n] & 1)) = hi;
+                    w -= f32x4{wkv7::bf16_lo(hi[0]), wkv7::bf16_hi(hi[0]), wkv7::bf16_lo(hi[1]),
+                               wkv7::bf16_hi(hi[1])};
+                    *reinterpret_cast<u32x2 *>(at + 1024 + 8 * (jt[n] & 1)) =
+                        u32x2{cvt_pk(w[0], w[1]), cvt_pk(w[2], w[3])};
+                } else {
+                    *reinterpret_cast<f32x4 *>(at + 1024 * (jt[n] & 1)) = w;
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            // S x^T
+            // S x^T; the next step's operand is formed beside this one's products
             constexpr int kRead = MODE == kGrad ? 3 : 2;
             f32x4 moved[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[i] = moved[i] = zero();
+            for (int i = 0; i < 4; ++i) {
+                moved[i] = zero();
+#pragma unroll
+                for (int n = 0; n < NT; ++n) out[n][i] = zero();
+            }
+            Frag<E> fx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fx[i] = PK::rows(x_rows, i, 0);
+            Parts<E, kRead> s(S[0][0], S[0][1]);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                Frag<E> fx[4];
+                Frag<E> fn[4];
+                if (ks + 1 < KS)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) fx[i] = tx.rows(tile_row(i, lo), 32 * ks, g);
-                const Parts<E, kRead> s(S[2 * ks], S[2 * ks + 1]);
+                    for (int i = 0; i < 4; ++i) fn[i] = PK::rows(x_rows, i, ks + 1);
 #pragma unroll
-                for (int part = s.kN - 1; part >= 0; --part)
+                for (int n = 0; n < NT; ++n) {
+                    const Parts<E, kRead> now = s;
+                    if (n + 1 < NT)
+                        s = Parts<E, kRead>(S[n + 1 < NT ? n + 1 : 0][2 * ks], S[n + 1 < NT ? n + 1 : 0][2 * ks + 1]);
+                    else if (ks + 1 < KS)
+                        s = Parts<E, kRead>(S[0][(2 * ks + 2) % M], S[0][(2 * ks + 3) % M]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) out[i] = mma(s.p[part], fx[i], out[i]);
-                if constexpr (MODE == kGrad) {
-                    const Parts<E, kRead> r(R[2 * ks], R[2 * ks + 1]);
+                    for (int part = now.kN - 1; part >= 0; --part)
 #pragma unroll
-                    for (int part = r.kN - 1; part >= 0; --part)
+                        for (int i = 0; i < 4; ++i) out[n][i] = mma(now.p[part], fx[i], out[n][i]);
+                    if constexpr (MODE == kGrad) {
+                        const Parts<E, kRead> r(R[2 * ks], R[2 * ks + 1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) moved[i] = mma(r.p[part], fx[i], moved[i]);
+                        for (int part = r.kN - 1; part >= 0; --part)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) moved[i] = mma(r.p[part], fx[i], moved[i]);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fx[i] = fn[i];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (MODE == kGrad) {
-                    const int t = tile_row(i, lo);
-                    const f32x4 m = moved[i] + (float)(t + 1) * out[i];
-                    const E *q = te.p + te.offset(t, own0 + 4 * g);
+                    const f32x4 m = moved[i] + (float)(16 * i + lo + 1) * out[0][i];
+                    const E *q = reinterpret_cast<const E *>(pe + own_place + 16 * i * PV::kRow);
                     float s = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s += to_float(q[e]) * m[e];
                     dg_chunk += rd[i] * s;
                 }
-                out[i] *= rd[i];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) out[n][i] *= rd[i];
             }
             __syncthreads();  // the fragments are whole
         }
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            if constexpr (MODE == kGrad) {
-                const f32x4 r = R[m] + (float)live * S[m];
-                R[m] = r * whole.hi + r * whole.lo;
-            }
-            S[m] = S[m] * whole.hi + S[m] * whole.lo;
-        }
         // z: as it is for the products with the fragments, weighted for the state
+        Frag<E> z[2][NT];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            const Frag<E> z = tz.template cols<4>(32 * st, own0, lane);
-            if constexpr (MODE != kSum)
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
-                for (int part = kPartsMixed<E> - 1; part >= 0; --part)
+            for (int n = 0; n < NT; ++n) z[st][n] = PV::cols(z_cols, st, 16 * n);
+        auto weighted = [&](int st, int n, f32x4(&w)[2]) {
+            const f32x4 kd0 = *reinterpret_cast<const f32x4 *>(write + 32 * st + 4 * g),
+                        kd1 = *reinterpret_cast<const f32x4 *>(write + 32 * st + 16 + 4 * g);
 #pragma unroll
-                    for (int f = 0; f < 6; ++f)
-                        if (kLowStep[f] == st)
-                            out[kLowTile[f]] =
-                                mma(z, get_frag<E>(frags + f * L::kFrag + 1024 * part, lane), out[kLowTile[f]]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < 4; ++j) {
+                w[0][j] = kd0[j] * z[st][n].at(j);
+                w[1][j] = kd1[j] * z[st][n].at(4 + j);
+            }
+        };
+        Parts<E, 3> zs[NT], zr;
+        auto split = [&](int st, Parts<E, 3>(&zs)[NT]) {
             f32x4 w[2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j >> 2][j & 3] = kd[st][j] * z.at(j);
-            const Parts<E, 3> zs(w[0], w[1]);
-            if constexpr (MODE == kGrad)
+            for (int n = 0; n < NT; ++n) {
+                weighted(st, n, w);
+                zs[n] = Parts<E, 3>(w[0], w[1]);
+            }
+            if constexpr (MODE == kGrad) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j >> 2][j & 3] *= (float)(live - p.shift - (32 * st + 8 * g + j));
-            const Parts<E, 3> zr(w[0], w[1]);
+                for (int j = 0; j < 8; ++j)
+                    w[j >> 2][j & 3] *= (float)(live - p.shift - (32 * st + 4 * g + (j < 4 ? j : 12 + j)));
+                zr = Parts<E, 3>(w[0], w[1]);
+            }
+        };
+        if constexpr (MODE != kSum) {
 #pragma unroll
-            for (int m0 = 0; m0 < M; m0 += L::kGroup) {
-                Frag<E> y[L::kGroup];
+            for (int st = 0; st < 2; ++st)
 #pragma unroll
-                for (int m = 0; m < L::kGroup; ++m)
-                    y[m] = ty.template cols<8>(32 * st, 32 * ((m0 + m) >> 1) + 4 * ((m0 + m) & 1), lane);
+                for (int part = kPartsMixed<E> - 1; part >= 0; --part) {
 #pragma unroll
-                for (int part = zs.kN - 1; part >= 0; --part)
+                    for (int f = 0; f < 6; ++f)
+                        if (kLowStep[f] == st) {
+                            const Frag<E> w = get_frag<E>(frags + f * L::kFrag + 1024 * part, 0);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                out[n][kLowTile[f]] = mma(z[st][n], w, out[n][kLowTile[f]]);
+                        }
+                    if (sizeof(E) == 4) __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+        split(0, zs);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if constexpr (MODE == kGrad) R[m] = (R[m] + (float)live * S[n][m]) * fade;
+                S[n][m] *= fade;
+            }
+        if constexpr (MODE != kSum && sizeof(O) == sizeof(E)) {
+            // out in the place of the wave's own columns of z
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    char *at = pz + own_place + 16 * i * PV::kRow + 16 * n * (int)sizeof(E);
+                    if constexpr (sizeof(E) == 2)
+                        *reinterpret_cast<u32x2 *>(at) =
+                            u32x2{cvt_pk(out[n][i][0], out[n][i][1]), cvt_pk(out[n][i][2], out[n][i][3])};
+                    else
+                        *reinterpret_cast<f32x4 *>(at) = out[n][i];
+                }
+        }
+        if constexpr (MODE != kSum && sizeof(O) != sizeof(E)) {
+            const Buffer b(op + start_of(c) * row, row_bytes<O>(live, row));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 16 * n + 4 * g, row, live, reverse),
+                             out[n][i], O());
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // the state, kGroup tiles of columns at a time; the next group's rows of y on their way
+        {
+            Frag<E> y[L::kGroup], yn[L::kGroup];
+            auto columns = [&](int at, Frag<E>(&y)[L::kGroup]) {
+#pragma unroll
+                for (int m = 0; m < L::kGroup; ++m) {
+                    const int col = at % M + m;
+                    y[m] = PK::cols(y_cols, at / M, 32 * (col >> 1) + 4 * (col & 1));
+                }
+            };
+            columns(0, y);
+#pragma unroll
+            for (int at = 0; at < 2 * M; at += L::kGroup) {
+                if (at + L::kGroup < 2 * M) columns(at + L::kGroup, yn);
+                const int m0 = at % M;
+                Parts<E, 3> zn[NT], zw = zr;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) zn[n] = zs[n];
+                if (at + L::kGroup == M) split(1, zs);
+#pragma unroll
+                for (int part = zw.kN - 1; part >= 0; --part)
 #pragma unroll
                     for (int m = 0; m < L::kGroup; ++m) {
-                        S[m0 + m] = mma(y[m], zs.p[part], S[m0 + m]);
-                        if constexpr (MODE == kGrad) R[m0 + m] = mma(y[m], zr.p[part], R[m0 + m]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) S[n][m0 + m] = mma(y[m], zn[n].p[part], S[n][m0 + m]);
+                        if constexpr (MODE == kGrad) R[m0 + m] = mma(y[m], zw.p[part], R[m0 + m]);
                     }
+#pragma unroll
+                for (int m = 0; m < L::kGroup; ++m) y[m] = yn[m];
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if constexpr (MODE != kSum) {
-            O *to = op + start_of(c) * row;
-            if constexpr (sizeof(O) == sizeof(E)) {
-                // in the place of the wave's own columns of z
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    E *at = tz.p + tz.offset(tile_row(i, lo), own0 + 4 * g);
-                    if constexpr (sizeof(E) == 2)
-                        *reinterpret_cast<u32x2 *>(at) =
-                            u32x2{cvt_pk(out[i][0], out[i][1]), cvt_pk(out[i][2], out[i][3])};
-                    else
-                        *reinterpret_cast<f32x4 *>(at) = out[i];
-                }
-                __syncthreads();  // out is whole, and x and y have been read
-                Rows<E, VD, kThreads>::store(tz, to, row, live, reverse, tid);
-            } else {
-                const Buffer b(to, row_bytes<O>(live, row));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b.store4(Rows<O, VD, kThreads>::offset(tile_row(i, lo), own0 + 4 * g, row, live, reverse),
-                             out[i], O());
-                __syncthreads();
-            }
-            if constexpr (MODE == kGrad) dg += dg_chunk;
-        } else {
-            __syncthreads();
-        }
+        __syncthreads();  // out is whole, and the planes have been read
+        if constexpr (MODE != kSum && sizeof(O) == sizeof(E))
+            Rows<E, VD, kThreads>::store(pz, reinterpret_cast<E *>(op + start_of(c) * row), row, live, reverse, tid);
+        if constexpr (MODE == kGrad) dg += dg_chunk;
         if (!L::kAhead) fetch(c + 1);
         put();
         __syncthreads();
@@ -485,7 +635,7 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dg += (double)(R[m][e] * S[m][e]);
+                for (int e = 0; e < 4; ++e) dg += (double)(R[m][e] * S[0][m][e]);
         }
 #pragma unroll
         for (int x = 32; x; x >>= 1) dg += __shfl_xor(dg, x);
@@ -509,8 +659,10 @@ __global__ __launch_bounds__(VD * 4, sizeof(E) == 2 ? 2 : 1) void pass_kernel(Pa
     }
     if (to)  // (only passes with states [VD, KD] leave one)
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-            *reinterpret_cast<f32x4 *>(to + (own0 + lo) * KD + tile_row(m, 4 * g)) = S[m];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                *reinterpret_cast<f32x4 *>(to + (own0 + 16 * n + lo) * KD + tile_row(m, 4 * g)) = S[n][m];
 }
 
 // From what the segments add to the states at their starts (in a reversed pass: at their
@@ -535,7 +687,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     const int len = sq.end - sq.begin, n = (len + a.seg - 1) / a.seg;
     const int at = (int)(blockIdx.x % parts * 256 + threadIdx.x) * 4;
     const Decay decay(a.g[h / a.parts]);
-    const Sum2 whole = decay.exact(a.seg), last = decay.exact(len - (n - 1) * a.seg);
+    const double whole = decay.exact(a.seg), last = decay.exact(len - (n - 1) * a.seg);
     f32x4 S = zero();
     if (p.s_in) {
         const int slot = p.slots ? p.slots[seq] : seq;
@@ -546,22 +698,24 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     float *u = p.units + ((size_t)sq.slot0 * a.heads + h) * a.state + at;
     // a sequence of no tokens has one segment of none
     const int count = n < 1 ? 1 : n;
-    for (int i0 = 0; i0 < count; i0 += 4) {
-        f32x4 add[4];
+    constexpr int kAtOnce = 8;
+    for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+        f32x4 add[kAtOnce];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < kAtOnce; ++x) {
             const int i = i0 + x;
             if (i < count - 1)
                 add[x] = *reinterpret_cast<const f32x4 *>(u + (p.reverse ? count - 1 - i : i) * step);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < kAtOnce; ++x) {
             const int i = i0 + x;
             if (i >= count) break;
             const int unit = p.reverse ? count - 1 - i : i;
             *reinterpret_cast<f32x4 *>(u + unit * step) = S;
-            const Sum2 d = p.reverse && i == 0 ? last : whole;
-            if (i < count - 1) S = S * d.hi + S * d.lo + add[x];
+            const double d = p.reverse && i == 0 ? last : whole;
+            const float hi = (float)d, lo = (float)(d - hi);  // (as exact as a product of floats is)
+            if (i < count - 1) S = S * hi + (S * lo + add[x]);
         }
     }
 }
@@ -607,7 +761,7 @@ hipError_t launch_pass(const PassArgs &a, int units, int passes, hipStream_t str
     const hipError_t e = allow_lds(kernel, L::kBytes);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((pass_kernel<E, O, KD, VD, MODE>),
-                       dim3((unsigned)((size_t)units * a.heads), (unsigned)passes), dim3(4 * VD), L::kBytes,
+                       dim3((unsigned)((size_t)units * a.heads), (unsigned)passes), dim3(L::kThreads), L::kBytes,
                        stream, a);
     return hipGetLastError();
 }
@@ -733,20 +887,27 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
         e = launch_combine(p, b.seg, b.g, ways, 2, stream);
         if (e != hipSuccess) return e;
     }
-    // ds_T and ds0 may be the same memory: dv, which writes ds0, is last
-    a.pass[0] = dq;
+    // dq (with dg in a kernel of its own), dk and dv, at once where the shapes and the types of
+    // their outputs are alike.  ds_T and ds0 may be the same memory: then dv, which writes ds0, is
+    // launched behind those that read ds_T.
+    const bool alike = p.K == p.V && (!wide || !p.bf16) && (b.seg.seg || b.ds0 != b.ds_T);
+    int n = 0;
     if (b.dg_units) {
+        a.pass[0] = dq;
         e = launch_pass<kGrad>(a, p.bf16, wide, p.V, p.K, units, 1, stream);
-        a.pass[0] = dk;
-        if (e == hipSuccess) e = launch_pass<kOut>(a, p.bf16, wide, p.V, p.K, units, 1, stream);
+        if (e != hipSuccess) return e;
     } else {
-        a.pass[1] = dk;
-        e = launch_pass<kOut>(a, p.bf16, wide, p.V, p.K, units, 2, stream);
+        a.pass[n++] = dq;
     }
+    a.pass[n++] = dk;
+    if (alike) a.pass[n++] = dv;
+    e = launch_pass<kOut>(a, p.bf16, wide, p.V, p.K, units, n, stream);
     if (e != hipSuccess) return e;
-    a.pass[0] = dv;
-    e = launch_pass<kOut>(a, p.bf16, false, p.K, p.V, units, 1, stream);
-    if (e != hipSuccess) return e;
+    if (!alike) {
+        a.pass[0] = dv;
+        e = launch_pass<kOut>(a, p.bf16, false, p.K, p.V, units, 1, stream);
+        if (e != hipSuccess) return e;
+    }
     if (b.dg) {
         hipLaunchKernelGGL(dg_kernel, dim3((unsigned)(p.heads / p.parts)), dim3(64), 0, stream, b.dg_units,
                            b.dg, units, p.heads, p.parts);
@@ -767,14 +928,30 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
     return e;
 }
 
-// (first form: whole sequences wherever they fill the card)
-Segments plan_segments(const Problem &p, bool) {
+// How a call's sequences are cut into segments, which are then done in parallel.  A segment's
+// sum and the combination cost about half of the pass again, so whole sequences are taken where
+// they fill the card (256 workgroups: a chunk takes 4.2 us alone on a CU and 8.3 us beside
+// another one; 8 x 4096 tokens, 40 heads of 64: 261 us whole, 249 in halves, 303 in 256s) or are
+// short (300 tokens, 32 heads of 128: 27 us whole, 31 in 64s).  Else about two workgroups per CU
+// (32768 tokens, 32 heads: 418 us in 2048s, 442 in 1024s, 470 in 512s), one in the backward,
+// whose chunks take longer (4096 tokens, 16 heads: 175 us in 256s, 210 in 128s), and not more
+// than the combination, a step of 0.25 us for each, is worth (6 us for a chunk more in each).
+// A packed batch's longest sequence, which the host does not know, is taken for twice the mean.
+Segments plan_segments(const Problem &p, bool backward) {
     Segments s{0, p.n_seq};
     const long long chains = (long long)p.n_seq * p.heads;
-    if (chains >= 1024 || p.total <= 256 || p.total <= 128 * p.n_seq) return s;
-    long long seg = (long long)p.total * p.heads / 1024;  // about 1024 units
-    seg = (seg / 256 + 1) * 256;
-    if (!p.cu && seg >= p.T) return s;
+    const long long mean = p.total / p.n_seq, longest = p.n_seq > 1 && p.cu ? 2 * mean : mean;
+    if (chains >= 256 || longest <= (p.bf16 && !backward ? 384 : 192)) return s;
+    const long long slots = backward ? 256 : 512;
+    long long chunks = (p.total * (long long)p.heads / slots + kChunk - 1) / kChunk;
+    if (chunks < 1) chunks = 1;
+    while (chunks * chunks * 1600 < longest) ++chunks;
+    if (!p.cu) {  // equal ones
+        const long long all = (p.T + kChunk - 1) / kChunk, n = (all + chunks - 1) / chunks;
+        if (n < 2) return s;
+        chunks = (all + n - 1) / n;
+    }
+    const long long seg = chunks * kChunk;
     if (seg >= p.total) return s;
     s.seg = (int)seg;
     s.units = p.cu ? p.total / s.seg + p.n_seq : p.n_seq * ((p.T + s.seg - 1) / s.seg);
