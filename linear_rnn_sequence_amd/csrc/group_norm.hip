@@ -10,8 +10,12 @@
 // Backward, with the same values formed again from x:
 //   dn = dy act(gate) or dy act'(n),  dgate = dy n act'(gate),  du = dn w,
 //   dx = rstd (du - mean(du) - u mean(du u)),   dw = sum over rows of dn u,  db = of dn.
-// A team keeps its group for several rows, whose sums of dw and db it writes as one row of the
+// Workgroups keep their groups for many rows, whose sums of dw and db they write as one row of the
 // workspace; sum_kernel adds those in a fixed order.
+//
+// What bounds it: memory.  32768 rows of 32 groups of 128 channels with a gate (bf16, 805 MB) take
+// 144 us, 5.6 TB/s, where a large copy reaches 6.6; the gradients of 8191 rows of 40 groups of 64
+// (210 MB) 41 us, 5.1 TB/s, in which the vector units are busy two thirds of the time.
 #include <stdint.h>
 
 #include <initializer_list>
@@ -33,7 +37,9 @@ struct Args {
     void *y, *dx, *dgate;
     float *sums;  // [chunks, 2, C]
     long long rows, x_stride, gate_stride;
-    int groups, size, act, per_team;  // per_team: rows of a team
+    int groups, size, act;
+    int per_team;  // rows of a team; backward: of a workgroup
+    int tile;      // backward: groups of a workgroup
     float eps, inv_size;
     bool rms;
 };
@@ -71,6 +77,26 @@ __device__ __forceinline__ void narrow(Raw<float, VEC> &r, const float (&x)[VEC]
     for (int i = 0; i < VEC; ++i) r.e[i] = x[i];
 }
 
+// a store of what nobody reads soon (2% of a large call)
+template <class V>
+__device__ __forceinline__ void put(V *p, const V &x) {
+    typedef unsigned u4 __attribute__((ext_vector_type(4)));
+    if constexpr (sizeof(V) == 16)
+        __builtin_nontemporal_store(__builtin_bit_cast(u4, x), reinterpret_cast<u4 *>(p));
+    else
+        *p = x;
+}
+// the lane's channels of weight or bias (one address for each piece of VEC, as wide loads)
+template <int VEC, int NV>
+__device__ __forceinline__ void channels(float (&x)[VEC * NV], const float *p, const int (&col)[NV],
+                                         float otherwise) {
+#pragma unroll
+    for (int i = 0; i < VEC * NV; ++i) x[i] = otherwise;
+    if (p)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) __builtin_memcpy(&x[v * VEC], p + col[v], VEC * sizeof(float));
+}
+
 // sigmoid; for outputs of 8 bits the hardware's exponential and reciprocal, 2^-22 off
 template <class E>
 __device__ __forceinline__ float sigmoid(float x) {
@@ -98,179 +124,171 @@ __device__ __forceinline__ void by_kind(int act, F f) {
         f(std::integral_constant<bool, false>());
 }
 
-// Which group, and which rows, a thread's team has; the lane's number in the team.
-template <int L>
-struct Place {
-    int group, lane;
-    long long first, end;  // rows
-    __device__ __forceinline__ Place(const Args &a) {
-        const unsigned team = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / L;
+// A lane's channels of its team's group.
+template <int VEC, int L, int NV, bool FULL>
+struct Lane {
+    int col[NV];      // first channels of its pieces (of the group's first one where there is none)
+    int lane, pieces;
+    __device__ __forceinline__ Lane(int group, int size) {
         lane = (int)(threadIdx.x % L);
-        group = (int)(team % (unsigned)a.groups);
-        first = (long long)(team / (unsigned)a.groups) * a.per_team;
-        end = first + a.per_team < a.rows ? first + a.per_team : a.rows;
+        pieces = size / VEC;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) col[v] = group * size + (has(v * VEC) ? v * L + lane : 0) * VEC;
     }
+    // whether there is an element i of the lane's
+    __device__ __forceinline__ bool has(int i) const { return FULL || i / VEC * L + lane < pieces; }
 };
 
-// the statistics of R rows at once, one chain of sums beside the other: afterwards x holds u
-template <int L, int N, int R, bool FULL>
-__device__ __forceinline__ void normalize(float (&x)[R][N], float (&rstd)[R], const bool (&has)[N],
+// the statistics of a row: afterwards x holds u
+template <int VEC, int L, int NV, bool FULL>
+__device__ __forceinline__ void normalize(float (&x)[VEC * NV], float &rstd, const Lane<VEC, L, NV, FULL> &at,
                                           const Args &a) {
-    float mean[R], var[R];
+    constexpr int N = VEC * NV;
+    float mean = 0.f, var = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        mean[r] = 0.f;
+    for (int i = 0; i < N; ++i) mean += x[i];
+    mean = a.rms ? 0.f : team_sum<L>(mean) * a.inv_size;
 #pragma unroll
-        for (int i = 0; i < N; ++i) mean[r] += x[r][i];
+    for (int i = 0; i < N; ++i) {
+        x[i] = at.has(i) ? x[i] - mean : 0.f;
+        var += x[i] * x[i];
     }
+    rstd = rsqrtf(team_sum<L>(var) * a.inv_size + a.eps);
 #pragma unroll
-    for (int r = 0; r < R; ++r) mean[r] = a.rms ? 0.f : team_sum<L>(mean[r]) * a.inv_size;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        var[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            x[r][i] = FULL || has[i] ? x[r][i] - mean[r] : 0.f;
-            var[r] += x[r][i] * x[r][i];
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rstd[r] = rsqrtf(team_sum<L>(var[r]) * a.inv_size + a.eps);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[r][i] *= rstd[r];
-    }
+    for (int i = 0; i < N; ++i) x[i] *= rstd;
 }
 
-template <class E, int VEC, int L, int NV, int R, bool GATE, bool FULL>
+// One row after the other, the next one on its way meanwhile.  What a team does once (its place,
+// weight and bias) takes as long as three rows: 32768 x 32 groups of 128 took 477 us with a team for
+// each row, 278 with two rows to a team, 181 with four.  Two or four rows at once are no faster
+// (161 and 160 us for 157).
+template <class E, int VEC, int L, int NV, bool GATE, bool FULL>
 __global__ __launch_bounds__(kThreads) void forward_kernel(Args a) {
     constexpr int N = VEC * NV;
     using V = Raw<E, VEC>;
-    const Place<L> at(a);
-    if (at.first >= a.rows) return;
-    const int pieces = a.size / VEC;
-    bool has[N];
-    int col[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int piece = v * L + at.lane;
-        col[v] = at.group * a.size + (FULL || piece < pieces ? piece : 0) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = FULL || piece < pieces;
-    }
-    const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate);
+    const unsigned team = (blockIdx.x * (unsigned)kThreads + threadIdx.x) / L;
+    const long long first = (long long)(team / (unsigned)a.groups) * a.per_team;
+    if (first >= a.rows) return;
+    const Lane<VEC, L, NV, FULL> at((int)(team % (unsigned)a.groups), a.size);
+    const int rows = (int)(a.rows - first < a.per_team ? a.rows - first : a.per_team);
     const long long C = (long long)a.groups * a.size;
-    V rx[R][NV], rg[R][NV];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const long long row = at.first + r < at.end ? at.first + r : at.first;
+    const E *xp = static_cast<const E *>(a.x) + first * a.x_stride,
+            *gp = static_cast<const E *>(a.gate) + (GATE ? first * a.gate_stride : 0);
+    E *yp = static_cast<E *>(a.y) + first * C;
+    V rx[NV], rg[NV];
+    auto fetch = [&]() {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            rx[r][v] = *reinterpret_cast<const V *>(xp + row * a.x_stride + col[v]);
-            if constexpr (GATE) rg[r][v] = *reinterpret_cast<const V *>(gp + row * a.gate_stride + col[v]);
+            rx[v] = *reinterpret_cast<const V *>(xp + at.col[v]);
+            if constexpr (GATE) rg[v] = *reinterpret_cast<const V *>(gp + at.col[v]);
         }
-    }
+    };
+    fetch();
     float w[N], b[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        w[i] = a.weight ? a.weight[col[i / VEC] + i % VEC] : 1.f;
-        b[i] = a.bias ? a.bias[col[i / VEC] + i % VEC] : 0.f;
-    }
-    float u[R][N], rstd[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[r][i] = FULL || has[i] ? widen(rx[r][i / VEC].e[i % VEC]) : 0.f;
-    normalize<L, N, R, FULL>(u, rstd, has, a);
+    channels<VEC, NV>(w, a.weight, at.col, 1.f);
+    channels<VEC, NV>(b, a.bias, at.col, 0.f);
     const bool silu = a.act == GROUP_NORM_SILU;
-    by_kind(a.act, [&](auto none) {
+    for (int row = 0; row < rows; ++row) {
+        float u[N], z[N], rstd;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (at.first + r >= at.end) break;
-            E *yp = static_cast<E *>(a.y) + (at.first + r) * C;
+        for (int i = 0; i < N; ++i) {
+            u[i] = at.has(i) ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
+            if constexpr (GATE) z[i] = widen(rg[i / VEC].e[i % VEC]);
+        }
+        if (row + 1 < rows) {  // (y may be x: not this row again)
+            xp += a.x_stride;
+            gp += GATE ? a.gate_stride : 0;
+            fetch();
+        }
+        normalize<VEC, L, NV, FULL>(u, rstd, at, a);
+        by_kind(a.act, [&](auto none) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 float y[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int k = v * VEC + i;
-                    const float n = u[r][k] * w[k] + b[k];
-                    const float z = GATE ? widen(rg[r][v].e[i]) : n;
-                    const float act = none ? z : activate<E>(z, silu);
+                    const float n = u[k] * w[k] + b[k];
+                    const float g = GATE ? z[k] : n;
+                    const float act = none ? g : activate<E>(g, silu);
                     y[i] = GATE ? n * act : act;
                 }
-                if (has[v * VEC]) {
+                if (at.has(v * VEC)) {
                     V out;
                     narrow(out, y);
-                    *reinterpret_cast<V *>(yp + col[v]) = out;
+                    put(reinterpret_cast<V *>(yp + at.col[v]), out);
                 }
             }
-        }
-    });
+        });
+        yp += C;
+    }
 }
 
+// A workgroup has a tile of neighbouring groups for a chunk of rows; its teams take turns with the
+// rows, keep the sums of dw and db in registers, and add them up in shared memory at the end, so that
+// a chunk leaves one row of the workspace.
 template <class E, int VEC, int L, int NV, bool GATE, bool FULL>
-__global__ __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) void backward_kernel(Args a) {
-    constexpr int N = VEC * NV;
+__global__ __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 4 : 1) void backward_kernel(Args a) {
+    constexpr int N = VEC * NV, kTeams = kThreads / L;
     using V = Raw<E, VEC>;
-    const Place<L> at(a);
-    if (at.first >= a.rows) return;
-    const int pieces = a.size / VEC;
-    bool has[N];
-    int col[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int piece = v * L + at.lane;
-        col[v] = at.group * a.size + (FULL || piece < pieces ? piece : 0) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) has[v * VEC + i] = FULL || piece < pieces;
-    }
-    const E *xp = static_cast<const E *>(a.x), *gp = static_cast<const E *>(a.gate),
-            *dp = static_cast<const E *>(a.dy);
+    __shared__ float shared[kThreads * (2 * N + 2)];
+    const int tiles = a.groups / a.tile, turns = kTeams / a.tile;
+    const int team = (int)threadIdx.x / L, turn = team / a.tile;
+    const Lane<VEC, L, NV, FULL> at((int)(blockIdx.x % (unsigned)tiles) * a.tile + team % a.tile, a.size);
+    const long long chunk = blockIdx.x / (unsigned)tiles, first = chunk * a.per_team + turn;
+    const long long end = (chunk + 1) * a.per_team < a.rows ? (chunk + 1) * a.per_team : a.rows;
+    const int rows = first < end ? (int)((end - first + turns - 1) / turns) : 0;
     const long long C = (long long)a.groups * a.size;
-    float w[N], b[N], dw[N], db[N];
+    const E *xp = static_cast<const E *>(a.x) + first * a.x_stride,
+            *gp = static_cast<const E *>(a.gate) + (GATE ? first * a.gate_stride : 0),
+            *dp = static_cast<const E *>(a.dy) + first * C;
+    E *dxp = static_cast<E *>(a.dx) + first * C, *dzp = static_cast<E *>(a.dgate) + (GATE ? first * C : 0);
+    float dw[N], db[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        w[i] = a.weight ? a.weight[col[i / VEC] + i % VEC] : 1.f;
-        b[i] = a.bias ? a.bias[col[i / VEC] + i % VEC] : 0.f;
-        dw[i] = db[i] = 0.f;
-    }
+    for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
     V rx[NV], rg[NV], rd[NV];
-    auto fetch = [&](long long row) {
-        if (row >= at.end) row = at.end - 1;
+    auto fetch = [&]() {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            rx[v] = *reinterpret_cast<const V *>(xp + row * a.x_stride + col[v]);
-            rd[v] = *reinterpret_cast<const V *>(dp + row * C + col[v]);
-            if constexpr (GATE) rg[v] = *reinterpret_cast<const V *>(gp + row * a.gate_stride + col[v]);
+            rx[v] = *reinterpret_cast<const V *>(xp + at.col[v]);
+            rd[v] = *reinterpret_cast<const V *>(dp + at.col[v]);
+            if constexpr (GATE) rg[v] = *reinterpret_cast<const V *>(gp + at.col[v]);
         }
     };
     const bool silu = a.act == GROUP_NORM_SILU;
-    fetch(at.first);
-    for (long long row = at.first; row < at.end; ++row) {
-        float u[1][N], rstd[1], gate[N], dy[N], dn[N], dz[N];
+    if (rows > 0) fetch();
+    float w[N], b[N];
+    channels<VEC, NV>(w, a.weight, at.col, 1.f);
+    channels<VEC, NV>(b, a.bias, at.col, 0.f);
+    for (int row = 0; row < rows; ++row) {
+        float u[N], rstd, gate[N], dy[N], dn[N], dz[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            u[0][i] = FULL || has[i] ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
-            dy[i] = FULL || has[i] ? widen(rd[i / VEC].e[i % VEC]) : 0.f;
+            u[i] = at.has(i) ? widen(rx[i / VEC].e[i % VEC]) : 0.f;
+            dy[i] = at.has(i) ? widen(rd[i / VEC].e[i % VEC]) : 0.f;
             if constexpr (GATE) gate[i] = widen(rg[i / VEC].e[i % VEC]);
         }
-        if (row + 1 < at.end) fetch(row + 1);  // (dx may be dy: not this row's again)
-        normalize<L, N, 1, FULL>(u, rstd, has, a);
+        if (row + 1 < rows) {  // (dx may be dy: not this row's again)
+            xp += turns * a.x_stride;
+            gp += GATE ? turns * a.gate_stride : 0;
+            dp += turns * C;
+            fetch();
+        }
+        normalize<VEC, L, NV, FULL>(u, rstd, at, a);
         float sum = 0.f, along = 0.f;
         by_kind(a.act, [&](auto none) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float n = u[0][i] * w[i] + b[i];
+                const float n = u[i] * w[i] + b[i];
                 float slope = 1.f, act = GATE ? gate[i] : n;
                 if constexpr (!none) act = activate<E>(act, silu, slope);
                 dn[i] = dy[i] * (GATE ? act : slope);
                 if constexpr (GATE) dz[i] = dy[i] * n * slope;
-                dw[i] += dn[i] * u[0][i];
+                dw[i] += dn[i] * u[i];
                 db[i] += dn[i];
-                dn[i] = FULL || has[i] ? dn[i] * w[i] : 0.f;
+                dn[i] = at.has(i) ? dn[i] * w[i] : 0.f;
                 sum += dn[i];
-                along += dn[i] * u[0][i];
+                along += dn[i] * u[i];
             }
         });
         sum = a.rms ? 0.f : team_sum<L>(sum) * a.inv_size;
@@ -281,29 +299,46 @@ __global__ __launch_bounds__(kThreads, VEC * NV <= 8 ? 4 : 1) void backward_kern
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int k = v * VEC + i;
-                d[i] = rstd[0] * (dn[k] - sum - u[0][k] * along);
+                d[i] = rstd * (dn[k] - sum - u[k] * along);
                 if constexpr (GATE) z[i] = dz[k];
             }
-            if (has[v * VEC]) {
+            if (at.has(v * VEC)) {
                 V out;
                 narrow(out, d);
-                *reinterpret_cast<V *>(static_cast<E *>(a.dx) + row * C + col[v]) = out;
+                put(reinterpret_cast<V *>(dxp + at.col[v]), out);
                 if constexpr (GATE) {
                     narrow(out, z);
-                    *reinterpret_cast<V *>(static_cast<E *>(a.dgate) + row * C + col[v]) = out;
+                    put(reinterpret_cast<V *>(dzp + at.col[v]), out);
                 }
             }
         }
+        dxp += turns * C;
+        dzp += GATE ? turns * C : 0;
     }
-    if (a.sums) {
-        float *s = a.sums + at.first / a.per_team * 2 * C;
+    if (!a.sums) return;
+    float *mine = shared + threadIdx.x * 4;  // piece j of a thread: 1024 floats further each
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (has[i]) {
-                s[col[i / VEC] + i % VEC] = dw[i];
-                s[C + col[i / VEC] + i % VEC] = db[i];
-            }
+    for (int i = 0; i < N; ++i) {
+        mine[i / 4 * (4 * kThreads) + i % 4] = dw[i];
+        mine[(N + i) / 4 * (4 * kThreads) + (N + i) % 4] = db[i];
     }
+    __syncthreads();
+    if (turn) return;
+    for (int t = 1; t < turns; ++t) {
+        const float *other = mine + t * a.tile * L * 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            dw[i] += other[i / 4 * (4 * kThreads) + i % 4];
+            db[i] += other[(N + i) / 4 * (4 * kThreads) + (N + i) % 4];
+        }
+    }
+    float *s = a.sums + chunk * 2 * C;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (at.has(v * VEC)) {
+            __builtin_memcpy(s + at.col[v], &dw[v * VEC], VEC * sizeof(float));
+            __builtin_memcpy(s + C + at.col[v], &db[v * VEC], VEC * sizeof(float));
+        }
 }
 
 // out[c] = sum over the chunks' rows of column c (a chunk: [2, C], dweight's and dbias')
@@ -331,10 +366,6 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float *sums, float *dwe
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// rows that the forward's teams have at once
-template <int NV>
-constexpr int kRows = NV == 1 ? 4 : NV == 2 ? 2 : 1;
-
 struct Shape {
     int L, nv;  // lanes of a team, 8 to 64, and pieces of a lane, both powers of two
 };
@@ -373,14 +404,25 @@ rwkv7_status check_problem(const group_norm_problem *in, Checked &c) {
     return RWKV7_OK;
 }
 
-// Rows of a team in the backward: few enough that the teams fill the card several times over,
-// so many that the sums they leave are few bytes beside the rows.
-int backward_rows(const Args &a) {
-    const Shape s = shape_of(a.size, 1);
-    const long long teams = 4096LL * 64 / (s.L < 8 ? 8 : s.L);  // of about eight waves a SIMD
-    long long n = a.rows * a.groups / teams;
-    n = n < 8 ? 8 : n > 64 ? 64 : n;
-    return (int)n;
+// Rows of a workgroup in the backward: about 1024 workgroups, all that the card holds at once, and
+// no fewer than four rows to a team (8191 x 40 groups of 64: 41 us, with 2048 workgroups 45; a
+// team that wrote its own sums: 58).  Whatever the alignment: the workspace's size goes by it.
+constexpr int kBlocks = 1024;
+// groups of a workgroup with teams of L lanes: a power of two that divides their number, a quarter
+// of its teams at most, so that at least four take turns with the rows where there are so many
+int tile_of(int groups, int L) {
+    int tile = 1;
+    while (tile * 2 <= kThreads / L / 4 && groups % (tile * 2) == 0) tile *= 2;
+    return tile;
+}
+int backward_rows(const Args &a, int esz) {
+    const int L = shape_of(a.size, a.size % (16 / esz) ? 1 : 16 / esz).L, tile = tile_of(a.groups, L);
+    const long long turns = kThreads / L / tile, most = (a.rows + 4 * turns - 1) / (4 * turns);
+    long long chunks = kBlocks / (a.groups / tile);
+    chunks = chunks > most ? most : chunks;
+    chunks = chunks < 1 ? 1 : chunks;
+    const long long n = (a.rows + chunks - 1) / chunks;
+    return (int)(n < 1 ? 1 : n);
 }
 long long chunks_of(const Args &a, int per_team) { return (a.rows + per_team - 1) / per_team; }
 
@@ -418,28 +460,31 @@ int piece(const Args &a, int esz, std::initializer_list<const void *> ps) {
 }
 
 template <class E, int VEC, int L, int NV, bool FULL>
-void (*kernel_of(const Args &a, bool backward, bool many))(Args) {
-    constexpr int R = kRows<NV>;
+void (*kernel_of(const Args &a, bool backward))(Args) {
     if (backward)
         return a.gate ? &backward_kernel<E, VEC, L, NV, true, FULL> : &backward_kernel<E, VEC, L, NV, false, FULL>;
-    if (many)
-        return a.gate ? &forward_kernel<E, VEC, L, NV, R, true, FULL> : &forward_kernel<E, VEC, L, NV, R, false, FULL>;
-    return a.gate ? &forward_kernel<E, VEC, L, NV, 1, true, FULL> : &forward_kernel<E, VEC, L, NV, 1, false, FULL>;
+    return a.gate ? &forward_kernel<E, VEC, L, NV, true, FULL> : &forward_kernel<E, VEC, L, NV, false, FULL>;
 }
 template <class E, int VEC, int L, int NV>
 hipError_t launch(Args a, bool backward, hipStream_t stream) {
-    // several rows of a team at once where there are teams enough without
-    constexpr int R = kRows<NV>;
-    const bool many = R > 1 && a.rows * a.groups * L >= 64LL * 8192;
     // teams without idle lanes (the usual sizes) need no masks
     void (*kernel)(Args) = nullptr;
     if constexpr (VEC * sizeof(E) == 16)
-        if (a.size == VEC * L * NV) kernel = kernel_of<E, VEC, L, NV, true>(a, backward, many);
-    if (!kernel) kernel = kernel_of<E, VEC, L, NV, false>(a, backward, many);
-    a.per_team = backward ? backward_rows(a) : many ? R : 1;
-    const long long teams = chunks_of(a, a.per_team) * a.groups;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((teams * L + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       stream, a);
+        if (a.size == VEC * L * NV) kernel = kernel_of<E, VEC, L, NV, true>(a, backward);
+    if (!kernel) kernel = kernel_of<E, VEC, L, NV, false>(a, backward);
+    unsigned blocks;
+    if (backward) {
+        a.per_team = backward_rows(a, (int)sizeof(E));
+        a.tile = tile_of(a.groups, L);
+        blocks = (unsigned)(chunks_of(a, a.per_team) * (a.groups / a.tile));
+    } else {
+        // as many rows of a team as leave 32 waves for a SIMD (so that every grid's threads fit 32
+        // bits, too): 32768 x 32 groups of 128 took 144 us, with sixteen waves 153, with eight 155
+        const long long rows = a.rows * a.groups * L / (64LL * 32768);
+        a.per_team = (int)(rows < 1 ? 1 : rows);
+        blocks = (unsigned)((chunks_of(a, a.per_team) * a.groups * L + kThreads - 1) / kThreads);
+    }
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 template <class E, int VEC>
@@ -465,11 +510,6 @@ hipError_t launch(const Args &a, int esz, int vec, bool backward, hipStream_t st
     return vec == 2 ? launch<uint16_t, 2>(a, backward, stream) : launch<uint16_t, 1>(a, backward, stream);
 }
 
-// every grid's extent in threads fits 32 bits
-bool grid_ok(const Args &a, long long chunks) {
-    return chunks * a.groups <= 0xffffffffLL / 64 - kThreads && chunks <= 0x7fffffffLL;
-}
-
 }  // namespace
 }  // namespace gnorm
 
@@ -480,7 +520,7 @@ extern "C" {
 size_t group_norm_backward_workspace(const group_norm_problem *in) {
     Checked c;
     if (check_problem(in, c) != RWKV7_OK) return 0;
-    return (size_t)chunks_of(c.a, backward_rows(c.a)) * 2 * c.a.groups * c.a.size * 4;
+    return (size_t)chunks_of(c.a, backward_rows(c.a, c.esz)) * 2 * c.a.groups * c.a.size * 4;
 }
 
 rwkv7_status group_norm_forward(const group_norm_problem *in, const void *x, const void *gate,
@@ -493,7 +533,6 @@ rwkv7_status group_norm_forward(const group_norm_problem *in, const void *x, con
     const size_t esz = (size_t)c.esz;
     if (!aligned(x, esz) || !aligned(gate, esz) || !aligned(y, esz) || !aligned(weight, 4) || !aligned(bias, 4))
         return RWKV7_ERR_ALIGN;
-    if (!grid_ok(a, a.rows)) return RWKV7_ERR_SHAPE;
     const long long C = (long long)a.groups * a.size;
     const size_t params = (size_t)C * 4;
     const bool in_place = y == x && a.x_stride == C;
@@ -523,9 +562,8 @@ rwkv7_status group_norm_backward(const group_norm_problem *in, const void *x, co
         if (!aligned(p, esz)) return RWKV7_ERR_ALIGN;
     for (const float *p : {weight, bias, (const float *)dweight, (const float *)dbias})
         if (!aligned(p, 4)) return RWKV7_ERR_ALIGN;
-    const int per_team = backward_rows(a);
+    const int per_team = backward_rows(a, c.esz);
     const long long chunks = chunks_of(a, per_team), C = (long long)a.groups * a.size;
-    if (!grid_ok(a, chunks)) return RWKV7_ERR_SHAPE;
     const bool sums = dweight || dbias;
     const size_t need = sums ? (size_t)chunks * 2 * C * 4 : 0;
     if (need && (!workspace || workspace_bytes < need)) return RWKV7_ERR_WORKSPACE;
