@@ -90,17 +90,18 @@ struct Parts {
     }
 };
 
-// A chunk's 64 rows of C channels in shared memory.  The rows are a few pieces of 16 bytes
-// longer than their channels, such that reads along 16 rows and down the columns of 16 meet
-// different banks (mostly: 16 bits and 12 words more, a transposing read takes 3 cycles for 2),
-// and so that every address is a lane's own plus a number known to the compiler, where a
-// swizzle has to be computed for each (a third of the kernel's vector instructions).
+// A chunk's 64 rows of C channels in shared memory.  The rows are eight words longer than their
+// channels: of all paddings that keep 16 bytes aligned those of 8 more than a multiple of 16
+// words are best for every kind of read here (16 bytes along 16 rows: 4.6 cycles a wave, where 12
+// words more take 8.1; transposing ones 4.1 for 6.1).  Every address is a lane's own plus a
+// number known to the compiler, where a swizzle has to be computed for each (a third of the
+// kernel's vector instructions).
 //
 // Contraction over tokens: element j of lane group g is the token 32 st + 4 g + j, for j >= 4
 // 32 st + 16 + 4 g + j - 4, which is how two result tiles of 16 tokens make up an operand.
 template <class E, int C>
 struct Plane {
-    static constexpr int kWords = C * (int)sizeof(E) / 4 + (sizeof(E) == 4 ? 4 : 12), kRow = 4 * kWords;
+    static constexpr int kWords = C * (int)sizeof(E) / 4 + 8, kRow = 4 * kWords;
     static constexpr int kBytes = kChunk * kRow;
     char *p;
     // a lane's place for reads along the rows: row lo, channels 8 g ..
@@ -145,6 +146,18 @@ struct Plane {
         return f;
     }
 };
+
+// Asks the scheduler for three vector instructions behind each of N matrix products: a product
+// keeps the matrix core busy for four of them, and a wave's instructions issue in order.
+template <class E, int N>
+__device__ __forceinline__ void interleave() {
+    if constexpr (sizeof(E) == 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+        }
+}
 
 // Rows of a chunk on their way from memory to a plane; in a reversed pass row r is the
 // live - 1 - r-th in memory.  Rows behind `live` are zeros.
@@ -328,6 +341,8 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                *const z_rows = pz + PV::along(g, lo), *const e_rows = pe + PV::along(g, lo);
     // channels own0 + 4 g .. of row lo
     const int own_place = lo * PV::kRow + (own0 + 4 * g) * (int)sizeof(E);
+    // channels own0 + 8 (g >> 1) .. of row lo, or of row 16 + lo for odd g
+    const int pair_place = (lo + 16 * (g & 1)) * PV::kRow + (own0 + 8 * (g >> 1)) * 2;
     char *const frags = lds + L::kP + lane * 16;
 
     auto live_of = [&](int c) {
@@ -385,7 +400,7 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
 
     for (int c = 0; c < chunks; ++c) {
         const int live = live_of(c);
-        if (L::kAhead) fetch(c + 1);
+        if (L::kAhead && MODE == kSum) fetch(c + 1);
         if (live < kChunk) {  // the last one (its other weights are read behind the next barrier)
             whole = rest_of;
             if (tid < kChunk) {
@@ -489,6 +504,7 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
 #pragma unroll
                             for (int i = 0; i < 4; ++i) moved[i] = mma(r.p[part], fx[i], moved[i]);
                     }
+                    interleave<E, 4 * Parts<E, kRead>::kN * (MODE == kGrad ? 2 : 1)>();
                     __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
@@ -508,6 +524,7 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                 for (int n = 0; n < NT; ++n) out[n][i] *= rd[i];
             }
             __syncthreads();  // the fragments are whole
+            if (L::kAhead) fetch(c + 1);  // (at the top its registers would be in the way above)
         }
         // z: as it is for the products with the fragments, weighted for the state
         Frag<E> z[2][NT];
@@ -524,19 +541,34 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                 w[1][j] = kd1[j] * z[st][n].at(4 + j);
             }
         };
-        Parts<E, 3> zs[NT], zr;
-        auto split = [&](int st, Parts<E, 3>(&zs)[NT]) {
+        // ([0] for the tokens of st 0, [1] of st 1)
+        Parts<E, 3> zs[2][NT], zr[2];
+        auto split = [&](int st, int n) {
             f32x4 w[2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                weighted(st, n, w);
-                zs[n] = Parts<E, 3>(w[0], w[1]);
-            }
+            weighted(st, n, w);
+            zs[st][n] = Parts<E, 3>(w[0], w[1]);
             if constexpr (MODE == kGrad) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     w[j >> 2][j & 3] *= (float)(live - p.shift - (32 * st + 4 * g + (j < 4 ? j : 12 + j)));
-                zr = Parts<E, 3>(w[0], w[1]);
+                zr[st] = Parts<E, 3>(w[0], w[1]);
+            }
+        };
+        auto decayed = [&](int m0) {  // a group of the state's tiles
+#pragma unroll
+            for (int m = m0; m < m0 + L::kGroup; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (MODE == kGrad) R[m] = (R[m] + (float)live * S[n][m]) * fade;
+                    S[n][m] *= fade;
+                }
+        };
+        Frag<E> y[L::kGroup], yn[L::kGroup];
+        auto columns = [&](int at, Frag<E>(&y)[L::kGroup]) {
+#pragma unroll
+            for (int m = 0; m < L::kGroup; ++m) {
+                const int col = at % M + m;
+                y[m] = PK::cols(y_cols, at / M, 32 * (col >> 1) + 4 * (col & 1));
             }
         };
         if constexpr (MODE != kSum) {
@@ -555,26 +587,34 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                     if (sizeof(E) == 4) __builtin_amdgcn_sched_barrier(0);
                 }
         }
-        split(0, zs);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                if constexpr (MODE == kGrad) R[m] = (R[m] + (float)live * S[n][m]) * fade;
-                S[n][m] *= fade;
-            }
+        for (int n = 0; n < NT; ++n) split(0, n);
+        decayed(0);
+        if (MODE != kSum) interleave<E, 12 * NT>();
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE != kSum && sizeof(O) == sizeof(E)) {
-            // out in the place of the wave's own columns of z
+            // out in the place of the wave's own columns of z (stores of the lanes' pieces from
+            // here, of 64 bytes a row and wave, took 281 us where whole rows take 254: 8 x 4096
+            // tokens, 40 heads of 64)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    char *at = pz + own_place + 16 * i * PV::kRow + 16 * n * (int)sizeof(E);
-                    if constexpr (sizeof(E) == 2)
-                        *reinterpret_cast<u32x2 *>(at) =
-                            u32x2{cvt_pk(out[n][i][0], out[n][i][1]), cvt_pk(out[n][i][2], out[n][i][3])};
-                    else
-                        *reinterpret_cast<f32x4 *>(at) = out[n][i];
+                for (int i = 0; i < 4; i += 2) {
+                    const f32x4 &x = out[n][i], &y = out[n][i + 1];
+                    if constexpr (sizeof(E) == 2) {
+                        // Neighbouring lane groups trade the halves of two tiles (v_permlane16_swap:
+                        // the odd ones' of its first operand for the even ones' of its second), so
+                        // that a lane has eight values of a token: even groups of tile i, odd ones
+                        // of i + 1.  (Writes of 8 bytes meet the same banks: 16 cycles for 5.)
+                        const auto u = __builtin_amdgcn_permlane16_swap(cvt_pk(x[0], x[1]), cvt_pk(y[0], y[1]), false, false);
+                        const auto v = __builtin_amdgcn_permlane16_swap(cvt_pk(x[2], x[3]), cvt_pk(y[2], y[3]), false, false);
+                        *reinterpret_cast<u32x4 *>(pz + pair_place + 16 * i * PV::kRow + 32 * n) =
+                            u32x4{u[0], v[0], u[1], v[1]};
+                    } else {
+                        char *at = pz + own_place + 16 * i * PV::kRow + 64 * n;
+                        *reinterpret_cast<f32x4 *>(at) = x;
+                        *reinterpret_cast<f32x4 *>(at + 16 * PV::kRow) = y;
+                    }
                 }
         }
         if constexpr (MODE != kSum && sizeof(O) != sizeof(E)) {
@@ -586,38 +626,30 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                     b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 16 * n + 4 * g, row, live, reverse),
                              out[n][i], O());
         }
-        __builtin_amdgcn_sched_barrier(0);
-        // the state, kGroup tiles of columns at a time; the next group's rows of y on their way
-        {
-            Frag<E> y[L::kGroup], yn[L::kGroup];
-            auto columns = [&](int at, Frag<E>(&y)[L::kGroup]) {
+        // the state, kGroup tiles of columns at a time; beside the products the next group's rows of y
+        // are on their way, its tiles are decayed, and the second half's z is split
+        columns(0, y);
+#pragma unroll
+        for (int at = 0; at < 2 * M; at += L::kGroup) {
+            const int m0 = at % M, st = at / M;
+            if (at + L::kGroup < 2 * M) columns(at + L::kGroup, yn);
+            if (at + L::kGroup < M) decayed(at + L::kGroup);
+            if (st == 0)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (n == at / L::kGroup || (at + L::kGroup == M && n > at / L::kGroup)) split(1, n);
+#pragma unroll
+            for (int part = Parts<E, 3>::kN - 1; part >= 0; --part)
 #pragma unroll
                 for (int m = 0; m < L::kGroup; ++m) {
-                    const int col = at % M + m;
-                    y[m] = PK::cols(y_cols, at / M, 32 * (col >> 1) + 4 * (col & 1));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) S[n][m0 + m] = mma(y[m], zs[st][n].p[part], S[n][m0 + m]);
+                    if constexpr (MODE == kGrad) R[m0 + m] = mma(y[m], zr[st].p[part], R[m0 + m]);
                 }
-            };
-            columns(0, y);
 #pragma unroll
-            for (int at = 0; at < 2 * M; at += L::kGroup) {
-                if (at + L::kGroup < 2 * M) columns(at + L::kGroup, yn);
-                const int m0 = at % M;
-                Parts<E, 3> zn[NT], zw = zr;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) zn[n] = zs[n];
-                if (at + L::kGroup == M) split(1, zs);
-#pragma unroll
-                for (int part = zw.kN - 1; part >= 0; --part)
-#pragma unroll
-                    for (int m = 0; m < L::kGroup; ++m) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) S[n][m0 + m] = mma(y[m], zn[n].p[part], S[n][m0 + m]);
-                        if constexpr (MODE == kGrad) R[m0 + m] = mma(y[m], zw.p[part], R[m0 + m]);
-                    }
-#pragma unroll
-                for (int m = 0; m < L::kGroup; ++m) y[m] = yn[m];
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int m = 0; m < L::kGroup; ++m) y[m] = yn[m];
+            interleave<E, L::kGroup * Parts<E, 3>::kN * (NT + (MODE == kGrad))>();
+            __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();  // out is whole, and the planes have been read
         if constexpr (MODE != kSum && sizeof(O) == sizeof(E))
