@@ -22,7 +22,7 @@
 // reads it out as it does S, and at the end takes its product with the cotangent.  (The usual
 // sum of position times q dq - k dk cancels to nothing for long sequences.)
 //
-// Layout: a wave owns 16 or 32 rows of the state over all KD columns, as matrix-core result
+// Layout: a wave owns 16 rows of the state over all KD columns, as matrix-core result
 // tiles [columns, rows]: S x^T and the products with z^T need nothing of another wave.  The
 // chunk's rows of x, y and z lie in shared memory; x y^T, six fragments of the lower
 // triangle, is computed by the waves together and passed through it.
@@ -147,6 +147,14 @@ struct Plane {
     }
 };
 
+// a value that is the same for all lanes, out of the vector registers
+__device__ __forceinline__ double uniform(double x) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)u),
+                   hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32));
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+
 // Asks the scheduler for three vector instructions behind each of N matrix products: a product
 // keeps the matrix core busy for four of them, and a wave's instructions issue in order.
 template <class E, int N>
@@ -224,30 +232,36 @@ struct Decay {
 
 template <class E, int KD, int VD, Mode MODE>
 struct Shared {
-    // Waves of a workgroup, and tiles of 16 rows of the state that each owns.
-    static constexpr int kOwn = sizeof(E) == 2 && MODE != kGrad && VD >= KD ? 2 : 1, kWaves = VD / 16 / kOwn;
-    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kWaves = VD / 16, kThreads = 64 * kWaves;
     static constexpr int kTileK = Plane<E, KD>::kBytes, kTileV = Plane<E, VD>::kBytes;
     static constexpr int kFrag = 2048;  // bf16: two parts, float: two halves
     static constexpr int kY = 0, kZ = kTileK, kX = kZ + kTileV;
     static constexpr int kP = kX + (MODE == kSum ? 0 : kTileK);
     static constexpr int kE = kP + (MODE == kSum ? 0 : 6 * kFrag);
-    // weights: of the tokens in the state [64], of pairs of tokens by their distance
-    // (-64 .. 63; 0 below 0)
+    // weights: of the tokens in the state [64], of pairs of tokens by their distance (-64 .. 63;
+    // 0 below 0), of the tokens' readouts [64]
     static constexpr int kWrite = kE + (MODE == kGrad ? kTileV : 0), kPair = kWrite + kChunk * 4;
-    static constexpr int kBytes = kPair + 2 * kChunk * 4;
+    static constexpr int kReads = kPair + 2 * kChunk * 4;
+    static constexpr int kBytes = kReads + kChunk * 4;
     // the next chunk's rows are on their way while this one is computed (in float they
     // would take the registers that its products need)
     static constexpr bool kAhead = sizeof(E) == 2 && !(MODE == kGrad && KD > VD);
+    // Waves per SIMD that the registers are shared out to.  Four (128 registers) hide what a wave
+    // waits for: 8 x 4096 tokens, 40 heads of 64, took 262 us with two waves of 32 rows of the state
+    // each and takes 215; 16 ragged sequences, 32 heads of 128, 158 and 150.
+    static constexpr int kPerSimd = sizeof(E) == 4 ? 1 : MODE == kGrad || KD > VD ? 2 : 4;
+    // where 128 registers are few, for two operands at a time and the weights of the readout
+    static constexpr bool kFew = kPerSimd == 4 && KD == 128 && MODE == kOut;
+    static constexpr bool kDouble = !kFew, kWeights = !kFew;
     // tiles of columns that the state's products have in registers at a time
-    static constexpr int kGroup = sizeof(E) == 4 || MODE == kGrad ? 2 : 4;
+    static constexpr int kGroup = 2;
 };
 
 template <class E, class O, int KD, int VD, Mode MODE>
-__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4 ? 1 : 2) void pass_kernel(
+__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD, VD, MODE>::kPerSimd)) void pass_kernel(
     PassArgs a) {
     using L = Shared<E, KD, VD, MODE>;
-    constexpr int W = L::kWaves, NT = L::kOwn, kThreads = L::kThreads, KS = KD / 32, M = KD / 16;
+    constexpr int W = L::kWaves, kThreads = L::kThreads, KS = KD / 32, M = KD / 16;
     constexpr int kTiles = (10 + W - 1) / W;  // of x y^T per wave
     extern __shared__ __align__(16) char lds[];
     const Pass &p = a.pass[blockIdx.y];
@@ -278,33 +292,30 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
     const size_t state_size = (size_t)VD * KD;
 
     const Decay decay(a.g[h / a.parts]);
-    float *write = reinterpret_cast<float *>(lds + L::kWrite), *pairs = reinterpret_cast<float *>(lds + L::kPair);
+    float *write = reinterpret_cast<float *>(lds + L::kWrite), *pairs = reinterpret_cast<float *>(lds + L::kPair),
+          *reads = reinterpret_cast<float *>(lds + L::kReads);
     if (tid < kChunk) {
         write[tid] = p.write * decay.power(kChunk - p.shift - tid);
         pairs[tid] = 0.f;
         pairs[kChunk + tid] = p.intra * decay.power(tid);
+        reads[tid] = p.read * decay.power(tid + p.shift);
     }
 
-    // the wave's rows of a state in memory: row own0 + 16 n + lo, columns tile_row(m, 4g) ..
-    const int own0 = 16 * NT * wave;
-    auto load_state = [&](f32x4(&S)[NT][M], const float *base) {
+    // the wave's rows of a state in memory: row own0 + lo, columns tile_row(m, 4g) ..
+    const int own0 = 16 * wave;
+    auto load_state = [&](f32x4(&S)[M], const float *base) {
         if (p.turned) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int m = 0; m < M; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[n][m][e] = base[(tile_row(m, 4 * g) + e) * VD + own0 + 16 * n + lo];
+                for (int e = 0; e < 4; ++e) S[m][e] = base[(tile_row(m, 4 * g) + e) * VD + own0 + lo];
         } else {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int m = 0; m < M; ++m)
-                    S[n][m] = *reinterpret_cast<const f32x4 *>(base + (own0 + 16 * n + lo) * KD + tile_row(m, 4 * g));
+            for (int m = 0; m < M; ++m)
+                S[m] = *reinterpret_cast<const f32x4 *>(base + (own0 + lo) * KD + tile_row(m, 4 * g));
         }
     };
-    f32x4 S[NT][M], R[MODE == kGrad ? M : 1];
+    f32x4 S[M], R[MODE == kGrad ? M : 1];
     const float *from = nullptr;
     if (MODE != kSum && a.seg) {
         from = p.unit_states + ((size_t)unit * a.heads + h) * state_size;
@@ -316,9 +327,7 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
         load_state(S, from);
     } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < M; ++m) S[n][m] = zero();
+        for (int m = 0; m < M; ++m) S[m] = zero();
     }
     if constexpr (MODE == kGrad)
 #pragma unroll
@@ -388,14 +397,15 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
             }
     __syncthreads();
 
-    float rd[4];  // weights of the readout of the tokens 16 i + lo
+    float rds[4];  // of the readout of the tokens 16 i + lo
+    if constexpr (L::kWeights)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rd[i] = p.read * decay.power(16 * i + lo + p.shift);
+        for (int i = 0; i < 4; ++i) rds[i] = p.read * decay.power(16 * i + lo + p.shift);
     // The state's decay over a chunk, as a float: what that is off by goes into the next one,
     // so that after any number of chunks the state has been decayed by the exact power.
-    double whole = decay.exact(kChunk), owed = 1.0;
-    const double rest_of = decay.exact(live_of(chunks - 1));  // over the last chunk
-    const double back = whole > 1e-30 ? 1.0 / whole : 0.0;
+    double whole = uniform(decay.exact(kChunk)), owed = 1.0;
+    const double rest_of = uniform(decay.exact(live_of(chunks - 1)));  // over the last chunk
+    const double back = uniform(whole > 1e-30 ? 1.0 / whole : 0.0);
     double dg = 0.0;
 
     for (int c = 0; c < chunks; ++c) {
@@ -411,8 +421,8 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
         }
         const double want = whole * owed;
         const float fade = (float)want;
-        owed = 1.0 + (want - fade) * back;
-        f32x4 out[NT][4];
+        owed = uniform(1.0 + (want - fade) * back);
+        f32x4 out[4];
         float dg_chunk = 0.f;
         if constexpr (MODE != kSum) {
             // x y^T, masked and decayed: tiles (it, jt) of the lower triangle, row by row; the waves
@@ -471,82 +481,68 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
             constexpr int kRead = MODE == kGrad ? 3 : 2;
             f32x4 moved[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                moved[i] = zero();
-#pragma unroll
-                for (int n = 0; n < NT; ++n) out[n][i] = zero();
-            }
+            for (int i = 0; i < 4; ++i) out[i] = moved[i] = zero();
             Frag<E> fx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) fx[i] = PK::rows(x_rows, i, 0);
-            Parts<E, kRead> s(S[0][0], S[0][1]);
+            Parts<E, kRead> s(S[0], S[1]);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 Frag<E> fn[4];
-                if (ks + 1 < KS)
+                if (L::kDouble && ks + 1 < KS)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) fn[i] = PK::rows(x_rows, i, ks + 1);
+                if (!L::kDouble && ks > 0)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const Parts<E, kRead> now = s;
-                    if (n + 1 < NT)
-                        s = Parts<E, kRead>(S[n + 1 < NT ? n + 1 : 0][2 * ks], S[n + 1 < NT ? n + 1 : 0][2 * ks + 1]);
-                    else if (ks + 1 < KS)
-                        s = Parts<E, kRead>(S[0][(2 * ks + 2) % M], S[0][(2 * ks + 3) % M]);
+                    for (int i = 0; i < 4; ++i) fx[i] = PK::rows(x_rows, i, ks);
+                const Parts<E, kRead> now = s;
+                if (ks + 1 < KS) s = Parts<E, kRead>(S[(2 * ks + 2) % M], S[(2 * ks + 3) % M]);
 #pragma unroll
-                    for (int part = now.kN - 1; part >= 0; --part)
+                for (int part = now.kN - 1; part >= 0; --part)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) out[n][i] = mma(now.p[part], fx[i], out[n][i]);
-                    if constexpr (MODE == kGrad) {
-                        const Parts<E, kRead> r(R[2 * ks], R[2 * ks + 1]);
+                    for (int i = 0; i < 4; ++i) out[i] = mma(now.p[part], fx[i], out[i]);
+                if constexpr (MODE == kGrad) {
+                    const Parts<E, kRead> r(R[2 * ks], R[2 * ks + 1]);
 #pragma unroll
-                        for (int part = r.kN - 1; part >= 0; --part)
+                    for (int part = r.kN - 1; part >= 0; --part)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) moved[i] = mma(r.p[part], fx[i], moved[i]);
-                    }
-                    interleave<E, 4 * Parts<E, kRead>::kN * (MODE == kGrad ? 2 : 1)>();
-                    __builtin_amdgcn_sched_barrier(0);
+                        for (int i = 0; i < 4; ++i) moved[i] = mma(r.p[part], fx[i], moved[i]);
                 }
+                interleave<E, 4 * Parts<E, kRead>::kN * (MODE == kGrad ? 2 : 1)>();
+                __builtin_amdgcn_sched_barrier(0);
+                if (L::kDouble)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) fx[i] = fn[i];
+                    for (int i = 0; i < 4; ++i) fx[i] = fn[i];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const float rd = L::kWeights ? rds[i] : reads[16 * i + lo];
                 if constexpr (MODE == kGrad) {
-                    const f32x4 m = moved[i] + (float)(16 * i + lo + 1) * out[0][i];
+                    const f32x4 m = moved[i] + (float)(16 * i + lo + 1) * out[i];
                     const E *q = reinterpret_cast<const E *>(pe + own_place + 16 * i * PV::kRow);
                     float s = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s += to_float(q[e]) * m[e];
-                    dg_chunk += rd[i] * s;
+                    dg_chunk += rd * s;
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) out[n][i] *= rd[i];
+                out[i] *= rd;
             }
             __syncthreads();  // the fragments are whole
             if (L::kAhead) fetch(c + 1);  // (at the top its registers would be in the way above)
         }
         // z: as it is for the products with the fragments, weighted for the state
-        Frag<E> z[2][NT];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) z[st][n] = PV::cols(z_cols, st, 16 * n);
-        auto weighted = [&](int st, int n, f32x4(&w)[2]) {
+        const Frag<E> z[2] = {PV::cols(z_cols, 0, 0), PV::cols(z_cols, 1, 0)};
+        Parts<E, 3> zs[2], zr[2];  // (by st)
+        auto split = [&](int st) {
+            f32x4 w[2];
             const f32x4 kd0 = *reinterpret_cast<const f32x4 *>(write + 32 * st + 4 * g),
                         kd1 = *reinterpret_cast<const f32x4 *>(write + 32 * st + 16 + 4 * g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                w[0][j] = kd0[j] * z[st][n].at(j);
-                w[1][j] = kd1[j] * z[st][n].at(4 + j);
+                w[0][j] = kd0[j] * z[st].at(j);
+                w[1][j] = kd1[j] * z[st].at(4 + j);
             }
-        };
-        // ([0] for the tokens of st 0, [1] of st 1)
-        Parts<E, 3> zs[2][NT], zr[2];
-        auto split = [&](int st, int n) {
-            f32x4 w[2];
-            weighted(st, n, w);
-            zs[st][n] = Parts<E, 3>(w[0], w[1]);
+            zs[st] = Parts<E, 3>(w[0], w[1]);
             if constexpr (MODE == kGrad) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -556,12 +552,10 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
         };
         auto decayed = [&](int m0) {  // a group of the state's tiles
 #pragma unroll
-            for (int m = m0; m < m0 + L::kGroup; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (MODE == kGrad) R[m] = (R[m] + (float)live * S[n][m]) * fade;
-                    S[n][m] *= fade;
-                }
+            for (int m = m0; m < m0 + L::kGroup; ++m) {
+                if constexpr (MODE == kGrad) R[m] = (R[m] + (float)live * S[m]) * fade;
+                S[m] *= fade;
+            }
         };
         Frag<E> y[L::kGroup], yn[L::kGroup];
         auto columns = [&](int at, Frag<E>(&y)[L::kGroup]) {
@@ -580,27 +574,22 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                     for (int f = 0; f < 6; ++f)
                         if (kLowStep[f] == st) {
                             const Frag<E> w = get_frag<E>(frags + f * L::kFrag + 1024 * part, 0);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                out[n][kLowTile[f]] = mma(z[st][n], w, out[n][kLowTile[f]]);
+                            out[kLowTile[f]] = mma(z[st], w, out[kLowTile[f]]);
                         }
                     if (sizeof(E) == 4) __builtin_amdgcn_sched_barrier(0);
                 }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) split(0, n);
+        split(0);
         decayed(0);
-        if (MODE != kSum) interleave<E, 12 * NT>();
+        if (MODE != kSum) interleave<E, 12>();
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE != kSum && sizeof(O) == sizeof(E)) {
             // out in the place of the wave's own columns of z (stores of the lanes' pieces from
             // here, of 64 bytes a row and wave, took 281 us where whole rows take 254: 8 x 4096
             // tokens, 40 heads of 64)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const f32x4 &x = out[n][i], &y = out[n][i + 1];
+            for (int i = 0; i < 4; i += 2) {
+                    const f32x4 &x = out[i], &y = out[i + 1];
                     if constexpr (sizeof(E) == 2) {
                         // Neighbouring lane groups trade the halves of two tiles (v_permlane16_swap:
                         // the odd ones' of its first operand for the even ones' of its second), so
@@ -608,10 +597,10 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
                         // of i + 1.  (Writes of 8 bytes meet the same banks: 16 cycles for 5.)
                         const auto u = __builtin_amdgcn_permlane16_swap(cvt_pk(x[0], x[1]), cvt_pk(y[0], y[1]), false, false);
                         const auto v = __builtin_amdgcn_permlane16_swap(cvt_pk(x[2], x[3]), cvt_pk(y[2], y[3]), false, false);
-                        *reinterpret_cast<u32x4 *>(pz + pair_place + 16 * i * PV::kRow + 32 * n) =
+                        *reinterpret_cast<u32x4 *>(pz + pair_place + 16 * i * PV::kRow) =
                             u32x4{u[0], v[0], u[1], v[1]};
                     } else {
-                        char *at = pz + own_place + 16 * i * PV::kRow + 64 * n;
+                        char *at = pz + own_place + 16 * i * PV::kRow;
                         *reinterpret_cast<f32x4 *>(at) = x;
                         *reinterpret_cast<f32x4 *>(at + 16 * PV::kRow) = y;
                     }
@@ -620,11 +609,8 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
         if constexpr (MODE != kSum && sizeof(O) != sizeof(E)) {
             const Buffer b(op + start_of(c) * row, row_bytes<O>(live, row));
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 16 * n + 4 * g, row, live, reverse),
-                             out[n][i], O());
+            for (int i = 0; i < 4; ++i)
+                b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 4 * g, row, live, reverse), out[i], O());
         }
         // the state, kGroup tiles of columns at a time; beside the products the next group's rows of y
         // are on their way, its tiles are decayed, and the second half's z is split
@@ -632,23 +618,21 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
 #pragma unroll
         for (int at = 0; at < 2 * M; at += L::kGroup) {
             const int m0 = at % M, st = at / M;
-            if (at + L::kGroup < 2 * M) columns(at + L::kGroup, yn);
+            if (L::kDouble && at + L::kGroup < 2 * M) columns(at + L::kGroup, yn);
+            if (!L::kDouble && at) columns(at, y);
             if (at + L::kGroup < M) decayed(at + L::kGroup);
-            if (st == 0)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (n == at / L::kGroup || (at + L::kGroup == M && n > at / L::kGroup)) split(1, n);
+            if (at == (L::kDouble ? 0 : M)) split(1);
 #pragma unroll
             for (int part = Parts<E, 3>::kN - 1; part >= 0; --part)
 #pragma unroll
                 for (int m = 0; m < L::kGroup; ++m) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) S[n][m0 + m] = mma(y[m], zs[st][n].p[part], S[n][m0 + m]);
+                    S[m0 + m] = mma(y[m], zs[st].p[part], S[m0 + m]);
                     if constexpr (MODE == kGrad) R[m0 + m] = mma(y[m], zr[st].p[part], R[m0 + m]);
                 }
+            if (L::kDouble)
 #pragma unroll
-            for (int m = 0; m < L::kGroup; ++m) y[m] = yn[m];
-            interleave<E, L::kGroup * Parts<E, 3>::kN * (NT + (MODE == kGrad))>();
+                for (int m = 0; m < L::kGroup; ++m) y[m] = yn[m];
+            interleave<E, L::kGroup * Parts<E, 3>::kN * (MODE == kGrad ? 2 : 1)>();
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();  // out is whole, and the planes have been read
@@ -667,7 +651,7 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dg += (double)(R[m][e] * S[0][m][e]);
+                for (int e = 0; e < 4; ++e) dg += (double)(R[m][e] * S[m][e]);
         }
 #pragma unroll
         for (int x = 32; x; x >>= 1) dg += __shfl_xor(dg, x);
@@ -691,10 +675,8 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), sizeof(E) == 4
     }
     if (to)  // (only passes with states [VD, KD] leave one)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-                *reinterpret_cast<f32x4 *>(to + (own0 + 16 * n + lo) * KD + tile_row(m, 4 * g)) = S[n][m];
+        for (int m = 0; m < M; ++m)
+            *reinterpret_cast<f32x4 *>(to + (own0 + lo) * KD + tile_row(m, 4 * g)) = S[m];
 }
 
 // From what the segments add to the states at their starts (in a reversed pass: at their
