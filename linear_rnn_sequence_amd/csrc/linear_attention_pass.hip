@@ -53,6 +53,7 @@ struct Pass {
     const int *slots_in, *slots_out;
     int pool;
     float *unit_states;                // segments: their starts (kSum: what they add)
+    bool direct;                       // sequences of one segment have theirs in s_in alone
     // kGrad
     const void *e;                     // rows of q
     int e_stride, e_rep;
@@ -258,13 +259,11 @@ struct Shared {
 };
 
 template <class E, class O, int KD, int VD, Mode MODE>
-__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD, VD, MODE>::kPerSimd)) void pass_kernel(
-    PassArgs a) {
+__device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
     using L = Shared<E, KD, VD, MODE>;
     constexpr int W = L::kWaves, kThreads = L::kThreads, KS = KD / 32, M = KD / 16;
     constexpr int kTiles = (10 + W - 1) / W;  // of x y^T per wave
     extern __shared__ __align__(16) char lds[];
-    const Pass &p = a.pass[blockIdx.y];
     const int tid = threadIdx.x, lane = tid & 63,
               wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, lo = lane & 15;
     const int unit = (int)(blockIdx.x / a.heads), h = (int)(blockIdx.x % a.heads);
@@ -317,7 +316,8 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD,
     };
     f32x4 S[M], R[MODE == kGrad ? M : 1];
     const float *from = nullptr;
-    if (MODE != kSum && a.seg) {
+    // (a sequence of one segment, whose state nobody else writes, starts from where it lies)
+    if (MODE != kSum && a.seg && !(p.direct && first == 0 && len == rest)) {
         from = p.unit_states + ((size_t)unit * a.heads + h) * state_size;
     } else if (MODE != kSum && p.s_in) {
         const int slot = p.slots_in ? p.slots_in[seq] : seq;
@@ -679,6 +679,21 @@ __global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD,
             *reinterpret_cast<f32x4 *>(to + (own0 + lo) * KD + tile_row(m, 4 * g)) = S[m];
 }
 
+template <class E, class O, int KD, int VD, Mode MODE>
+__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD, VD, MODE>::kPerSimd)) void pass_kernel(
+    PassArgs a) {
+    run_pass<E, O, KD, VD, MODE>(a, a.pass[blockIdx.y]);
+}
+// dq with dg, and the passes behind it, in one launch
+template <class E, class O, int KD, int VD>
+__global__ __launch_bounds__((Shared<E, KD, VD, kGrad>::kThreads), (Shared<E, KD, VD, kGrad>::kPerSimd)) void
+gradient_kernel(PassArgs a) {
+    if (blockIdx.y == 0)
+        run_pass<E, O, KD, VD, kGrad>(a, a.pass[0]);
+    else
+        run_pass<E, O, KD, VD, kOut>(a, a.pass[blockIdx.y]);
+}
+
 // From what the segments add to the states at their starts (in a reversed pass: at their
 // ends), in place: start of the next = decay over this one * start of this one + what it adds.
 struct CombineArgs {
@@ -690,7 +705,7 @@ struct CombineArgs {
         const float *s_in;
         const int *slots;
         int pool;
-        bool reverse;
+        bool reverse, direct;
     } way[2];  // by blockIdx.y
 };
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
@@ -700,6 +715,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     const Seq sq = a.lay.seq(seq, a.seg);
     const int len = sq.end - sq.begin, n = (len + a.seg - 1) / a.seg;
     const int at = (int)(blockIdx.x % parts * 256 + threadIdx.x) * 4;
+    if (p.direct && n < 2) return;
     const Decay decay(a.g[h / a.parts]);
     const double whole = decay.exact(a.seg), last = decay.exact(len - (n - 1) * a.seg);
     f32x4 S = zero();
@@ -712,15 +728,21 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     float *u = p.units + ((size_t)sq.slot0 * a.heads + h) * a.state + at;
     // a sequence of no tokens has one segment of none
     const int count = n < 1 ? 1 : n;
+    // eight segments' at a time, the next eight on their way before these are overwritten
     constexpr int kAtOnce = 8;
-    for (int i0 = 0; i0 < count; i0 += kAtOnce) {
-        f32x4 add[kAtOnce];
+    f32x4 add[kAtOnce], next[kAtOnce];
+    auto fetch = [&](int i0) {
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const int i = i0 + x;
-            if (i < count - 1)
-                add[x] = *reinterpret_cast<const f32x4 *>(u + (p.reverse ? count - 1 - i : i) * step);
-        }
+        for (int x = 0; x < kAtOnce; ++x)
+            if (i0 + x < count - 1)
+                next[x] = *reinterpret_cast<const f32x4 *>(
+                    u + (p.reverse ? count - 1 - i0 - x : i0 + x) * step);
+    };
+    fetch(0);
+    for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) add[x] = next[x];
+        fetch(i0 + kAtOnce);
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
             const int i = i0 + x;
@@ -734,33 +756,43 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     }
 }
 
-// dg of the caller's heads from the units', in a fixed order
-__global__ __launch_bounds__(64) void dg_kernel(const double *units, float *dg, int n, int heads,
-                                                int parts) {
-    const int h0 = (int)blockIdx.x * parts;
-    double s = 0.0;
-    for (long long i = threadIdx.x; i < (long long)n * parts; i += 64)
-        s += units[i / parts * heads + h0 + i % parts];
-    for (int x = 32; x; x >>= 1) s += __shfl_xor(s, x);
-    if (threadIdx.x == 0) dg[blockIdx.x] = (float)s;
-}
-
-// the gradient of a key head's rows: the sum over the heads that read it.  A workgroup has the
-// rows of one chunk (rows outside every sequence are nobody's).
+// What is left of the gradients: dg of the caller's heads from the units', in a fixed order
+// (blockIdx.y 0), and the gradient of a key head's rows, the sum over the heads that read it (1: of
+// q, 2: of k).  There a workgroup has the rows of one chunk; rows outside every sequence are
+// nobody's.
+struct RestArgs {
+    Layout lay;
+    const double *units;
+    float *dg;
+    int n, heads, parts;
+    const float *dq, *dk;
+    void *out_q, *out_k;
+    int rep, Hk, K, chunks;  // 0 chunks: no shared heads
+};
 template <class E>
-__global__ __launch_bounds__(256) void shared_kernel(Layout lay, const float *dq, const float *dk,
-                                                     E *out_q, E *out_k, int rep, int Hk, int K) {
+__global__ __launch_bounds__(256) void rest_kernel(RestArgs a) {
+    if (blockIdx.y == 0) {
+        const int head = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);  // a wave each
+        if (!a.dg || head >= a.heads / a.parts) return;
+        double s = 0.0;
+        for (long long i = threadIdx.x & 63; i < (long long)a.n * a.parts; i += 64)
+            s += a.units[i / a.parts * a.heads + head * a.parts + i % a.parts];
+        for (int x = 32; x; x >>= 1) s += __shfl_xor(s, x);
+        if ((threadIdx.x & 63) == 0) a.dg[head] = (float)s;
+        return;
+    }
+    if ((int)blockIdx.x >= a.chunks) return;  // many heads, few tokens
     Seq sq;
-    lay.find((int)blockIdx.x, kChunk, sq);
+    a.lay.find((int)blockIdx.x, kChunk, sq);
     const long long first = (long long)sq.begin + (long long)((int)blockIdx.x - sq.slot0) * kChunk;
     if ((int)blockIdx.x < sq.slot0 || first >= sq.end) return;
-    const int rows = sq.end - first < kChunk ? (int)(sq.end - first) : kChunk, row = Hk * K;
-    const float *src = (blockIdx.y ? dk : dq) + first * rep * row;
-    E *dst = (blockIdx.y ? out_k : out_q) + first * row;
+    const int rows = sq.end - first < kChunk ? (int)(sq.end - first) : kChunk, row = a.Hk * a.K;
+    const float *src = (blockIdx.y == 2 ? a.dk : a.dq) + first * a.rep * row;
+    E *dst = static_cast<E *>(blockIdx.y == 2 ? a.out_k : a.out_q) + first * row;
     for (long long i = threadIdx.x * 4; i < (long long)rows * row; i += 1024) {
-        const float *s = src + i / K * rep * K + i % K;
+        const float *s = src + i / a.K * a.rep * a.K + i % a.K;
         f32x4 sum = *reinterpret_cast<const f32x4 *>(s);
-        for (int r = 1; r < rep; ++r) sum += *reinterpret_cast<const f32x4 *>(s + (size_t)r * K);
+        for (int r = 1; r < a.rep; ++r) sum += *reinterpret_cast<const f32x4 *>(s + (size_t)r * a.K);
         if constexpr (sizeof(E) == 2)
             *reinterpret_cast<u32x2 *>(dst + i) = u32x2{cvt_pk(sum[0], sum[1]), cvt_pk(sum[2], sum[3])};
         else
@@ -777,6 +809,16 @@ hipError_t launch_pass(const PassArgs &a, int units, int passes, hipStream_t str
     hipLaunchKernelGGL((pass_kernel<E, O, KD, VD, MODE>),
                        dim3((unsigned)((size_t)units * a.heads), (unsigned)passes), dim3(L::kThreads), L::kBytes,
                        stream, a);
+    return hipGetLastError();
+}
+template <int D>
+hipError_t launch_gradients(const PassArgs &a, int units, hipStream_t stream) {
+    using L = Shared<float, D, D, kGrad>;
+    const hipError_t e =
+        allow_lds(reinterpret_cast<const void *>(&gradient_kernel<float, float, D, D>), L::kBytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gradient_kernel<float, float, D, D>), dim3((unsigned)((size_t)units * a.heads), 3),
+                       dim3(L::kThreads), L::kBytes, stream, a);
     return hipGetLastError();
 }
 template <class E, class O, Mode MODE>
@@ -834,10 +876,11 @@ hipError_t launch_forward(const ForwardArgs &f, hipStream_t stream) {
     w.s_in = f.s0; w.s_out = f.s_out;
     w.slots_in = p.slots_in; w.slots_out = p.slots_out; w.pool = p.pool;
     w.unit_states = f.states;
+    w.direct = true;
     if (f.seg.seg) {
         hipError_t e = launch_pass<kSum>(a, p.bf16, false, p.K, p.V, f.seg.units, 1, stream);
         if (e != hipSuccess) return e;
-        const CombineArgs::Way way{f.states, f.s0, p.slots_in, p.pool, false};
+        const CombineArgs::Way way{f.states, f.s0, p.slots_in, p.pool, false, true};
         e = launch_combine(p, f.seg, f.g, &way, 1, stream);
         if (e != hipSuccess) return e;
     }
@@ -896,17 +939,20 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
         a.pass[1] = dv;
         e = launch_pass<kSum>(a, p.bf16, false, p.K, p.V, units, 2, stream);
         if (e != hipSuccess) return e;
-        const CombineArgs::Way ways[2] = {{b.states, b.s0, nullptr, p.n_seq, false},
-                                          {b.cotangents, b.ds_T, nullptr, p.n_seq, true}};
+        const CombineArgs::Way ways[2] = {{b.states, b.s0, nullptr, p.n_seq, false, false},
+                                          {b.cotangents, b.ds_T, nullptr, p.n_seq, true, false}};
         e = launch_combine(p, b.seg, b.g, ways, 2, stream);
         if (e != hipSuccess) return e;
     }
-    // dq (with dg in a kernel of its own), dk and dv, at once where the shapes and the types of
-    // their outputs are alike.  ds_T and ds0 may be the same memory: then dv, which writes ds0, is
+    // dq, dk and dv, at once where the shapes and the types of their outputs are alike.  dq with dg
+    // is a launch of its own in bf16, where it has half as many waves on a SIMD as the others; in
+    // float they are equal.  ds_T and ds0 may be the same memory: then dv, which writes ds0, is
     // launched behind those that read ds_T.
     const bool alike = p.K == p.V && (!wide || !p.bf16) && (b.seg.seg || b.ds0 != b.ds_T);
     int n = 0;
-    if (b.dg_units) {
+    if (b.dg_units && alike && !p.bf16) {
+        a.pass[n++] = dq;
+    } else if (b.dg_units) {
         a.pass[0] = dq;
         e = launch_pass<kGrad>(a, p.bf16, wide, p.V, p.K, units, 1, stream);
         if (e != hipSuccess) return e;
@@ -915,28 +961,28 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
     }
     a.pass[n++] = dk;
     if (alike) a.pass[n++] = dv;
-    e = launch_pass<kOut>(a, p.bf16, wide, p.V, p.K, units, n, stream);
+    if (b.dg_units && n == 3)
+        e = p.K == 64 ? launch_gradients<64>(a, units, stream) : launch_gradients<128>(a, units, stream);
+    else
+        e = launch_pass<kOut>(a, p.bf16, wide, p.V, p.K, units, n, stream);
     if (e != hipSuccess) return e;
     if (!alike) {
         a.pass[0] = dv;
         e = launch_pass<kOut>(a, p.bf16, false, p.K, p.V, units, 1, stream);
         if (e != hipSuccess) return e;
     }
-    if (b.dg) {
-        hipLaunchKernelGGL(dg_kernel, dim3((unsigned)(p.heads / p.parts)), dim3(64), 0, stream, b.dg_units,
-                           b.dg, units, p.heads, p.parts);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (wide && p.total > 0) {
-        const unsigned chunks = (unsigned)(p.cu ? p.total / kChunk + p.n_seq
-                                                : p.n_seq * ((p.T + kChunk - 1) / kChunk));
+    int chunks = 0;
+    if (wide && p.total > 0)
+        chunks = p.cu ? p.total / kChunk + p.n_seq : p.n_seq * ((p.T + kChunk - 1) / kChunk);
+    if (b.dg || chunks) {
+        const RestArgs r{a.lay, b.dg_units, b.dg, units, p.heads, p.parts, b.dq_heads, b.dk_heads,
+                         b.dq, b.dk, p.rep(), p.Hk, p.K, chunks};
+        const int heads = b.dg ? (p.heads / p.parts + 3) / 4 : 0;
+        const dim3 grid((unsigned)(chunks > heads ? chunks : heads), chunks ? 3 : 1);
         if (p.bf16)
-            hipLaunchKernelGGL((shared_kernel<bf16_t>), dim3(chunks, 2), dim3(256), 0, stream, a.lay, b.dq_heads,
-                               b.dk_heads, static_cast<bf16_t *>(b.dq), static_cast<bf16_t *>(b.dk), p.rep(), p.Hk, p.K);
+            hipLaunchKernelGGL((rest_kernel<bf16_t>), grid, dim3(256), 0, stream, r);
         else
-            hipLaunchKernelGGL((shared_kernel<float>), dim3(chunks, 2), dim3(256), 0, stream, a.lay, b.dq_heads,
-                               b.dk_heads, static_cast<float *>(b.dq), static_cast<float *>(b.dk), p.rep(), p.Hk, p.K);
+            hipLaunchKernelGGL((rest_kernel<float>), grid, dim3(256), 0, stream, r);
         e = hipGetLastError();
     }
     return e;
@@ -960,6 +1006,10 @@ Segments plan_segments(const Problem &p, bool backward) {
     long long chunks = (p.total * (long long)p.heads / slots + kChunk - 1) / kChunk;
     if (chunks < 1) chunks = 1;
     while (chunks * chunks * 1600 < longest) ++chunks;
+    // (where most sequences are shorter, there are more of them: 16 up to 2049 tokens, 8 heads, took
+    // 82 us in 192s, 72 in 512s; 8 up to 1024, 16 heads, with gradients 203 in 192s, 169 in 256s)
+    if (p.cu && p.n_seq > 1 && p.bf16 && chunks * kChunk * 3 < 2 * mean)
+        chunks = (2 * mean / 3 + kChunk - 1) / kChunk;
     if (!p.cu) {  // equal ones
         const long long all = (p.T + kChunk - 1) / kChunk, n = (all + chunks - 1) / chunks;
         if (n < 2) return s;

@@ -360,6 +360,20 @@ def test_empty_batches(rnn, dtype):
         assert torch.equal(grads[4], s0) and not dg.any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T", [(1, 1), (1, 70), (2, 64), (3, 5)])
+def test_many_heads_of_one_key_head_over_few_tokens(rnn, dtype, B, T):
+    """More heads than chunks: what is summed over heads stays within the tokens."""
+    x = inputs(B * T, 1, 64, 64, 64, dtype, 12, B)
+    d_o = torch.from_numpy(np.random.default_rng(13).normal(size=(B, T, 64, 64))).to(DT[dtype]).cuda()
+    room = [torch.full((B * T + 4096, *t.shape[2:]), 7.0, dtype=DT[dtype], device="cuda") for t in x[:3]]
+    grads = [t[2048:2048 + B * T].view(B, T, *t.shape[1:]) for t in room]
+    got = rnn.linear_attention_backward(*x, d_o, grads=grads)
+    check_gradients(got, x, d_o, None, None, dtype, [(b, 0, T) for b in range(B)])
+    for t in room:
+        assert (t[:2048] == 7).all() and (t[2048 + B * T:] == 7).all()
+
+
 def test_gradient_of_the_state_in_place(rnn):
     for T in (100, 700):
         x, ds = inputs(T, 1, 2, 64, 128, "bf16", 5), states(1, 2, 128, 64, 6)
