@@ -15,7 +15,7 @@
 //
 // What bounds it: memory.  32768 rows of 32 groups of 128 channels with a gate (bf16, 805 MB) take
 // 144 us, 5.6 TB/s, where a large copy reaches 6.6; the gradients of 8191 rows of 40 groups of 64
-// (210 MB) 41 us, 5.1 TB/s, in which the vector units are busy two thirds of the time.
+// (210 MB) 39 us, 5.4 TB/s, in which the vector units are busy two thirds of the time.
 #include <stdint.h>
 
 #include <initializer_list>
@@ -341,7 +341,9 @@ __global__ __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 4 : 1) void backwar
         }
 }
 
-// out[c] = sum over the chunks' rows of column c (a chunk: [2, C], dweight's and dbias')
+// out[c] = sum over the chunks' rows of column c (a chunk: [2, C], dweight's and dbias').  A wave adds
+// every sixteenth row in turn, eight of them on their way at a time (8191 rows of 40 groups of 64:
+// 39.2 us for the gradients, 40.9 with each row waited for).
 __global__ __launch_bounds__(1024) void sum_kernel(const float *sums, float *dweight, float *dbias,
                                                    int chunks, int C) {
     __shared__ float part[16][64];
@@ -349,7 +351,8 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float *sums, float *dwe
     const long long c = (long long)blockIdx.x * 64 + lane;
     float s = 0.f;
     if (c < 2LL * C)
-        for (long long i = wave; i < chunks; i += 16) s += sums[i * 2 * C + c];
+#pragma unroll 8
+        for (int i = wave; i < chunks; i += 16) s += sums[(long long)i * 2 * C + c];
     part[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && c < 2LL * C) {
@@ -405,9 +408,12 @@ rwkv7_status check_problem(const group_norm_problem *in, Checked &c) {
 }
 
 // Rows of a workgroup in the backward: about 1024 workgroups, all that the card holds at once, and
-// no fewer than four rows to a team (8191 x 40 groups of 64: 41 us, with 2048 workgroups 45; a
-// team that wrote its own sums: 58).  Whatever the alignment: the workspace's size goes by it.
-constexpr int kBlocks = 1024;
+// no fewer than four rows to a team (4096 x 32 groups of 128: 31.0 us, with 2048 workgroups 31.8,
+// with 512 39); twice as many where a team would have more than 32 rows, since they do not end
+// together (32768 x 32 groups of 128: 262 us for 283).  A team that wrote its own sums made the
+// gradients of 8191 x 40 groups of 64 take 58 us for 41.  Whatever the alignment: the workspace's
+// size goes by it.
+constexpr int kBlocks = 1024, kManyRows = 32;
 // groups of a workgroup with teams of L lanes: a power of two that divides their number, a quarter
 // of its teams at most, so that at least four take turns with the rows where there are so many
 int tile_of(int groups, int L) {
@@ -419,6 +425,7 @@ int backward_rows(const Args &a, int esz) {
     const int L = shape_of(a.size, a.size % (16 / esz) ? 1 : 16 / esz).L, tile = tile_of(a.groups, L);
     const long long turns = kThreads / L / tile, most = (a.rows + 4 * turns - 1) / (4 * turns);
     long long chunks = kBlocks / (a.groups / tile);
+    if (a.rows > chunks * turns * kManyRows) chunks *= 2;
     chunks = chunks > most ? most : chunks;
     chunks = chunks < 1 ? 1 : chunks;
     const long long n = (a.rows + chunks - 1) / chunks;
