@@ -24,9 +24,10 @@ struct Problem {
     int rep() const { return heads / Hk; }  // heads that read the same key head
 };
 
-// Sequences in segments of `seg` tokens (0: whole), `units` of them at most.
+// Sequences in segments of `seg` tokens (0: whole), `units` of them at most; few to each sequence.
 struct Segments {
     int seg, units;
+    bool few;
 };
 Segments plan_segments(const Problem &p, bool backward);
 

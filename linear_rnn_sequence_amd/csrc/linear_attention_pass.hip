@@ -72,6 +72,7 @@ struct Pass {
 struct PassArgs {
     Layout lay;
     int seg, heads, parts;
+    bool join;  // segments take their starts from the sums of those before them, not from combine_kernel
     const float *g;
     Pass pass[3];  // by blockIdx.y
 };
@@ -291,7 +292,7 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
     } else {
         sq = a.lay.seq(unit, kChunk);
     }
-    const int rest = sq.end - sq.begin - first, len = a.seg && rest > a.seg ? a.seg : rest;
+    const int tokens = sq.end - sq.begin, rest = tokens - first, len = a.seg && rest > a.seg ? a.seg : rest;
     const bool ends = reverse ? first == 0 : len == rest, starts = reverse ? len == rest : first == 0;
     if (MODE == kSum && ends) return;  // nothing follows it
     const long long token = (long long)sq.begin + first;
@@ -322,15 +323,36 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
                 S[m] = *reinterpret_cast<const f32x4 *>(base + (own0 + lo) * KD + tile_row(m, 4 * g));
         }
     };
+    // The state at the segment's start (`back`: the cotangent at its end), where the segments are
+    // joined here: the sequence's own, and on top of it what the segments before (behind) add.
+    auto joined = [&](f32x4(&S)[M], const float *start, const float *units, bool back) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) S[m] = zero();
+        if (start) load_state(S, start);
+        const int all = tokens > a.seg ? (tokens + a.seg - 1) / a.seg : 1, mine = unit - sq.slot0;
+        const int before = back ? all - 1 - mine : mine;
+#pragma unroll 1
+        for (int i = 0; i < before; ++i) {
+            const int other = sq.slot0 + (back ? all - 1 - i : i);
+            const double d = uniform(decay.exact(back && i == 0 ? tokens - (all - 1) * a.seg : a.seg));
+            const float hi = (float)d, lo = (float)(d - hi);
+            f32x4 add[M];
+            load_state(add, units + ((size_t)other * a.heads + h) * state_size);
+#pragma unroll
+            for (int m = 0; m < M; ++m) S[m] = S[m] * hi + (S[m] * lo + add[m]);
+        }
+    };
     f32x4 S[M], R[MODE == kGrad ? M : 1];
     const float *from = nullptr;
-    if (MODE != kSum && a.seg && !(starts && p.direct >= (ends ? kAlone : kStart))) {
+    if (MODE != kSum && a.seg && !a.join && !(starts && p.direct >= (ends ? kAlone : kStart))) {
         from = p.unit_states + ((size_t)unit * a.heads + h) * state_size;
     } else if (MODE != kSum && p.s_in) {
         const int slot = p.slots_in ? p.slots_in[seq] : seq;
         if (slot >= 0 && slot < p.pool) from = p.s_in + ((size_t)slot * a.heads + h) * state_size;
     }
-    if (from) {
+    if (MODE != kSum && a.join) {
+        joined(S, from, p.unit_states, reverse);
+    } else if (from) {
         load_state(S, from);
     } else {
 #pragma unroll
@@ -659,8 +681,13 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
     if constexpr (MODE == kGrad) {
         // <R, cotangent>, and the sum over the workgroup, always in the same order
         const bool own = a.seg && !(ends && p.direct_end);
-        if (const float *D = own ? p.unit_cotangents : p.cotangent) {
-            load_state(S, D + ((size_t)(own ? unit : seq) * a.heads + h) * state_size);
+        const float *D = own && !a.join ? p.unit_cotangents : p.cotangent;
+        if (D) D += ((size_t)(own && !a.join ? unit : seq) * a.heads + h) * state_size;
+        if (D || (own && a.join)) {
+            if (a.join)
+                joined(S, D, p.unit_cotangents, true);
+            else
+                load_state(S, D);
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -895,8 +922,9 @@ hipError_t launch_forward(const ForwardArgs &f, hipStream_t stream) {
     if (f.seg.seg) {
         hipError_t e = launch_pass<kSum>(a, p.bf16, false, p.K, p.V, f.seg.units, 1, stream);
         if (e != hipSuccess) return e;
+        a.join = f.seg.few && w.direct == kStart;
         const CombineArgs::Way way{f.states, f.s0, p.slots_in, p.pool, false, w.direct};
-        e = launch_combine(p, f.seg, f.g, &way, 1, stream);
+        if (!a.join) e = launch_combine(p, f.seg, f.g, &way, 1, stream);
         if (e != hipSuccess) return e;
     }
     return launch_pass<kOut>(a, p.bf16, false, p.K, p.V, f.seg.units, 1, stream);
@@ -962,7 +990,8 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
         if (e != hipSuccess) return e;
         const CombineArgs::Way ways[2] = {{b.states, b.s0, nullptr, p.n_seq, false, kStart},
                                           {b.cotangents, b.ds_T, nullptr, p.n_seq, true, from_end}};
-        e = launch_combine(p, b.seg, b.g, ways, 2, stream);
+        a.join = b.seg.few && from_end == kStart;
+        if (!a.join) e = launch_combine(p, b.seg, b.g, ways, 2, stream);
         if (e != hipSuccess) return e;
     }
     // dq, dk and dv, at once where the shapes and the types of their outputs are alike.  dq with dg
@@ -1009,6 +1038,12 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
     return e;
 }
 
+// Dense sequences of at most this many segments are joined by the passes themselves, each reading
+// the sums before its own (1.1 us for one), without a combination: 4 x 2048 tokens, 32 heads of 128,
+// with gradients (4 segments forward, 2 backward) 398 us for 410; 8 segments of 512 tokens, 4 heads,
+// would take 31.6 for 23.4.
+constexpr int kFewSegments = 4;
+
 // How a call's sequences are cut into segments, which are then done in parallel.  A segment's
 // sum and the combination cost about half of the pass again, so whole sequences are taken where
 // they fill the card (256 workgroups: a chunk takes 4.2 us alone on a CU and 8.3 us beside
@@ -1019,7 +1054,7 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
 // than the combination, a step of 0.25 us for each, is worth (6 us for a chunk more in each).
 // A packed batch's longest sequence, which the host does not know, is taken for twice the mean.
 Segments plan_segments(const Problem &p, bool backward) {
-    Segments s{0, p.n_seq};
+    Segments s{0, p.n_seq, false};
     const long long chains = (long long)p.n_seq * p.heads;
     const long long mean = p.total / p.n_seq, longest = p.n_seq > 1 && p.cu ? 2 * mean : mean;
     if (chains >= 256 || longest <= (p.bf16 && !backward ? 384 : 192)) return s;
@@ -1035,6 +1070,7 @@ Segments plan_segments(const Problem &p, bool backward) {
         const long long all = (p.T + kChunk - 1) / kChunk, n = (all + chunks - 1) / chunks;
         if (n < 2) return s;
         chunks = (all + n - 1) / n;
+        s.few = n <= kFewSegments;
     }
     const long long seg = chunks * kChunk;
     if (seg >= p.total) return s;

@@ -192,7 +192,7 @@ def linear_attention_backward(q, k, v, g, d_o, s0=None, ds_T=None, *, cu_seqlens
     """linear_attention_backward.  Returns (dq, dk, dv, dg, ds0): the gradients of
     sum_t <o_t, d_o_t> + <S_T, ds_T> for the inputs of :func:`linear_attention_forward` (give the same
     s0, cu_seqlens and scale).  ``want_dg=False`` for decays that are not learned saves a fifth of
-    the call and returns None there; ``grads`` may pass the tensors for (dq, dk, dv); ``ds0`` may be
+    a large call and returns None there; ``grads`` may pass the tensors for (dq, dk, dv); ``ds0`` may be
     ``ds_T`` (in place).  Rows of a packed batch outside every sequence are not written."""
     import torch
 

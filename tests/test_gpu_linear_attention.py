@@ -193,6 +193,32 @@ def test_segments_against_float64(rnn, layout, T):
             close(a, f64(b), dtype, n)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V,started", [(64, 64, True), (64, 128, False), (128, 64, True)])
+def test_a_few_segments_to_a_sequence(rnn, dtype, K, V, started):
+    """Four in the forward, two in the backward, the last one shorter; from states and from none."""
+    B, T, Hk, Hv = 3, 430, 2, 46
+    x = inputs(B * T, Hk, Hv, K, V, dtype, 21, B)
+    x[3][0], x[3][1] = 0.0, -1e-3
+    s0, ds = (states(B, Hv, V, K, 3), states(B, Hv, V, K, 4)) if started else (None, None)
+    o, s = rnn.linear_attention_forward(*x, s0=s0)
+    for b in range(B):
+        want, S, _ = la.forward(*rows(x, b, 0, T), None if s0 is None else f64(s0[b]))
+        close(o[b], want, dtype, "o")
+        close(s[b], S, "f32", "state")
+    d_o = torch.from_numpy(np.random.default_rng(22).normal(size=(B, T, Hv, V))).to(DT[dtype]).cuda()
+    grads = rnn.linear_attention_backward(*x, d_o, s0, ds)
+    check_gradients(grads, x, d_o, ds, s0, dtype, [(b, 0, T) for b in range(B)])
+    if started:  # in place: the starts lie where the ends are written
+        pool, out = s0.clone(), ds.clone()
+        o2, s2 = rnn.linear_attention_forward(*x, s0=pool, s_out=pool)
+        close(o2, f64(o), dtype, "o in place")
+        close(s2, f64(s), "f32", "state in place")
+        for a, b, n in zip(rnn.linear_attention_backward(*x, d_o, s0, out, ds0=out), grads, ("dq", "dk", "dv", "", "ds0")):
+            if n:
+                close(a, f64(b), dtype, n)
+
+
 @pytest.mark.parametrize("layout", LAYOUTS, ids=str)
 @pytest.mark.parametrize("T", [1, 33, 64, 100, 150])
 def test_gradients(rnn, layout, T):
