@@ -26,6 +26,13 @@
 // tiles [columns, rows]: S x^T and the products with z^T need nothing of another wave.  The
 // chunk's rows of x, y and z lie in shared memory; x y^T, six fragments of the lower
 // triangle, is computed by the waves together and passed through it.
+//
+// What bounds it: the instructions of a chunk, of which the products of states in two and three
+// bf16 parts are the largest share.  32768 tokens of 32 heads of 128 x 128 take 390 to 410 us (243 the
+// pass, 126 the segments' sums, 12 their combination; 1.1 GB at 4.6 TB/s in the pass): matrix cores are
+// busy 45% of the time, vector units 39%, shared memory 51%, waves wait 38% of theirs.  A chunk
+// takes 4.2 us of a CU, also where a batch's longest sequence is a chain of them (16 ragged
+// sequences of up to 2049 tokens: 152 to 162 us, 33 chunks).
 #include "gated_delta_device.h"
 #include "linear_attention_internal.h"
 
@@ -1046,13 +1053,14 @@ constexpr int kFewSegments = 4;
 
 // How a call's sequences are cut into segments, which are then done in parallel.  A segment's
 // sum and the combination cost about half of the pass again, so whole sequences are taken where
-// they fill the card (256 workgroups: a chunk takes 4.2 us alone on a CU and 8.3 us beside
-// another one; 8 x 4096 tokens, 40 heads of 64: 261 us whole, 249 in halves, 303 in 256s) or are
-// short (300 tokens, 32 heads of 128: 27 us whole, 31 in 64s).  Else about two workgroups per CU
-// (32768 tokens, 32 heads: 418 us in 2048s, 442 in 1024s, 470 in 512s), one in the backward,
-// whose chunks take longer (4096 tokens, 16 heads: 175 us in 256s, 210 in 128s), and not more
-// than the combination, a step of 0.25 us for each, is worth (6 us for a chunk more in each).
-// A packed batch's longest sequence, which the host does not know, is taken for twice the mean.
+// they fill the card (256 workgroups; 8 x 4096 tokens, 40 heads of 64: 217 us whole, 255 in halves,
+// 296 in 256s) or are short (300 tokens, 32 heads of 128: 26 us whole, 30 in 64s, 25 in 128s).  Else
+// about two workgroups per CU (32768 tokens, 32 heads of 128: 402 us in 2048s, 424 in 1024s and in
+// 4096s, 460 in 512s), one in the backward, whose chunks take longer (4 x 2048 tokens, 32 heads:
+// 391 us in 1024s, 450 in 512s, 477 whole; 4096 tokens, 16 heads: 161 in 256s, 187 in 512s, 203 in
+// 128s), and not more than the combination, a step of 0.25 us for each, is worth (6 us for a chunk
+// more in each).  A packed batch's longest sequence, which the host does not know, is taken for
+// twice the mean.
 Segments plan_segments(const Problem &p, bool backward) {
     Segments s{0, p.n_seq, false};
     const long long chains = (long long)p.n_seq * p.heads;
@@ -1062,8 +1070,8 @@ Segments plan_segments(const Problem &p, bool backward) {
     long long chunks = (p.total * (long long)p.heads / slots + kChunk - 1) / kChunk;
     if (chunks < 1) chunks = 1;
     while (chunks * chunks * 1600 < longest) ++chunks;
-    // (where most sequences are shorter, there are more of them: 16 up to 2049 tokens, 8 heads, took
-    // 82 us in 192s, 72 in 512s; 8 up to 1024, 16 heads, with gradients 203 in 192s, 169 in 256s)
+    // (where most sequences are shorter, there are more of them: 16 up to 2049 tokens, 8 heads, take
+    // 77 us in 192s, 69 in 512s; 8 up to 1024, 16 heads, with gradients 191 in 192s, 157 in 256s)
     if (p.cu && p.n_seq > 1 && p.bf16 && chunks * kChunk * 3 < 2 * mean)
         chunks = (2 * mean / 3 + kChunk - 1) / kChunk;
     if (!p.cu) {  // equal ones
