@@ -1047,27 +1047,29 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
 
 // Dense sequences of at most this many segments are joined by the passes themselves, each reading
 // the sums before its own (1.1 us for one), without a combination: 4 x 2048 tokens, 32 heads of 128,
-// with gradients (4 segments forward, 2 backward) 398 us for 410; 8 segments of 512 tokens, 4 heads,
-// would take 31.6 for 23.4.
+// with gradients, in quarters forward and halves backward, take 398 us for 410; 8 segments of 512
+// tokens, 4 heads, would take 31.6 for 23.4.
 constexpr int kFewSegments = 4;
 
 // How a call's sequences are cut into segments, which are then done in parallel.  A segment's
 // sum and the combination cost about half of the pass again, so whole sequences are taken where
 // they fill the card (256 workgroups; 8 x 4096 tokens, 40 heads of 64: 217 us whole, 255 in halves,
 // 296 in 256s) or are short (300 tokens, 32 heads of 128: 26 us whole, 30 in 64s, 25 in 128s).  Else
-// about two workgroups per CU (32768 tokens, 32 heads of 128: 402 us in 2048s, 424 in 1024s and in
-// 4096s, 460 in 512s), one in the backward, whose chunks take longer (4 x 2048 tokens, 32 heads:
-// 391 us in 1024s, 450 in 512s, 477 whole; 4096 tokens, 16 heads: 161 in 256s, 187 in 512s, 203 in
-// 128s), and not more than the combination, a step of 0.25 us for each, is worth (6 us for a chunk
-// more in each).  A packed batch's longest sequence, which the host does not know, is taken for
-// twice the mean.
+// about one workgroup per CU (2 x 1000 tokens, 32 heads of 128: 44 us, with two per CU 55; 2 x 4096:
+// 109 and 115; with gradients, 4 x 2048: 391 in 1024s, 450 in 512s, 477 whole; 4096 tokens, 16 heads:
+// 161 in 256s, 187 in 512s, 203 in 128s).  In the forward two, where one would have more than 2048
+// tokens (32768 tokens, 32 heads of 128: 402 us in 2048s, 424 in 4096s and in 1024s, 460 in 512s) or
+// has four waves (2 x 4096, 40 heads of 64: 64 us, with one per CU 73).  And not more segments than
+// their combination, a step of 0.25 us for each, is worth (6 us for a chunk more in each).  A packed
+// batch's longest sequence, which the host does not know, is taken for twice the mean.
 Segments plan_segments(const Problem &p, bool backward) {
     Segments s{0, p.n_seq, false};
     const long long chains = (long long)p.n_seq * p.heads;
     const long long mean = p.total / p.n_seq, longest = p.n_seq > 1 && p.cu ? 2 * mean : mean;
     if (chains >= 256 || longest <= (p.bf16 && !backward ? 384 : 192)) return s;
-    const long long slots = backward ? 256 : 512;
-    long long chunks = (p.total * (long long)p.heads / slots + kChunk - 1) / kChunk;
+    const long long share = p.total * (long long)p.heads / 256;
+    const bool one = backward || (p.V == 128 && share <= 2048);  // workgroup per CU
+    long long chunks = ((one ? share : share / 2) + kChunk - 1) / kChunk;
     if (chunks < 1) chunks = 1;
     while (chunks * chunks * 1600 < longest) ++chunks;
     // (where most sequences are shorter, there are more of them: 16 up to 2049 tokens, 8 heads, take

@@ -196,7 +196,7 @@ def test_segments_against_float64(rnn, layout, T):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("K,V,started", [(64, 64, True), (64, 128, False), (128, 64, True)])
 def test_a_few_segments_to_a_sequence(rnn, dtype, K, V, started):
-    """Four in the forward, two in the backward, the last one shorter; from states and from none."""
+    """Two or four in the forward, two in the backward, the last one shorter; from states and from none."""
     B, T, Hk, Hv = 3, 430, 2, 46
     x = inputs(B * T, Hk, Hv, K, V, dtype, 21, B)
     x[3][0], x[3][1] = 0.0, -1e-3
@@ -346,6 +346,24 @@ def test_strided_inputs_of_a_joint_projection(rnn, dtype):
     a = rnn.linear_attention_decode(*(t[:, 5].contiguous() for t in x[:3]), x[3], pool)
     b = rnn.linear_attention_decode(*(t[:, 5] for t in views), x[3], pool2)
     assert torch.equal(a, b) and torch.equal(pool, pool2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_strides(rnn, dtype):
+    """2^23 elements from token to token: a chunk's rows lie over 2 GiB."""
+    T, Hk, Hv, K, V = 67, 1, 2, 64, 64
+    x = inputs(T, Hk, Hv, K, V, dtype, 31)
+    wide = torch.empty(T, 1 << 23, device="cuda", dtype=DT[dtype])
+    parts, at = [], (1 << 23) - 64 * 4
+    for t, n in zip(x[:3], (64, 64, 128)):
+        parts.append(wide[:, at:at + n].view(1, T, n // 64, 64))
+        parts[-1].copy_(t)
+        at += n
+    d_o = torch.from_numpy(np.random.default_rng(32).normal(size=(1, T, Hv, V))).to(DT[dtype]).cuda()
+    for a, b in zip(rnn.linear_attention_forward(*parts, x[3]), rnn.linear_attention_forward(*x)):
+        assert torch.equal(a, b)
+    for a, b in zip(rnn.linear_attention_backward(*parts, x[3], d_o), rnn.linear_attention_backward(*x, d_o)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("name", ["q", "k", "v", "g"])
