@@ -41,7 +41,8 @@
  *    products of the rows of a 64-token chunk with 16 bits (dg with 24), and are rounded once.
  *    The same call gives the same bits.
  *    Long sequences may be computed in segments, whose length depends on the sequences and
- *    heads of the call, so a sequence's last bits may depend on what else the call holds.
+ *    heads of the call, so a sequence's last bits may depend on what else the call holds, and on
+ *    whether its states are updated in place.
  *  - A workspace serves one call at a time: calls, or captured graphs, that may run at once
  *    need one each.  What it held before does not matter.
  *  - Non-finite inputs propagate within a (sequence, value head) pair, and from q and k to all

@@ -138,6 +138,12 @@ def test_many_rows(rnn, dtype, rows, groups, size):
     check(rnn, x, groups, dy, kw, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_for_twice_the_workgroups(rnn, dtype):
+    x, dy, kw = inputs(17001, 64, 8, dtype)
+    check(rnn, x, 64, dy, kw, dtype)
+
+
 def test_only_one_of_weight_and_bias(rnn):
     x, dy, kw = inputs(20, 3, 64, "f32")
     for n, i in (("weight", 1), ("bias", 2)):
