@@ -29,6 +29,9 @@
  *    access outside a buffer.
  *  - q, k and v may be strided from token to token (a slice of a joint projection); the
  *    channels of one token are dense [heads, K or V].
+ *  - The states of n_seq sequences take less than 2^38 bytes (also where none are given); Hv * V,
+ *    and Hv * K times the parts of at most 128 values that V is computed in (192: three of 64), are
+ *    at most 2^23.  Larger calls return RWKV7_ERR_SHAPE.
  *  - States s0, s_out are float32 [pool, Hv, V, K].  Without slots, sequence i has state i
  *    (pool = n_seq).  With slots (int32 [n_seq] on the device) sequence i starts from state
  *    slots_in[i] and leaves its final state in slots_out[i].  A slot outside [0, pool) stands

@@ -133,10 +133,12 @@ rwkv7_status check_problem(const linear_attention_problem *in, Problem &p, Sizes
     z.b_dk = z.b_dq + up256(rows);
     z.b_dg = z.b_dk + up256(rows);
     z.bwd = z.b_dg + dg;
-    // every grid's extent in threads fits 32 bits
-    const size_t most = 0xffffffffu / 512;
-    if ((size_t)z.fseg.units * p.heads > most || (size_t)z.bseg.units * p.heads > most ||
-        (size_t)p.n_seq * p.heads > most / 32)
+    // Every grid's extent in threads fits 32 bits: of the passes, 16 rows of a state a wave, and of
+    // single tokens, 16 numbers of a state a thread.  (A combination of segments, 4 a thread, is
+    // launched for fewer than 256 sequences and heads only.)
+    const size_t threads = 4 * (size_t)(p.V > p.K ? p.V : p.K), most = 0xffffffffu;
+    if ((size_t)z.fseg.units * p.heads > most / threads ||
+        (size_t)z.bseg.units * p.heads > most / threads || z.states / 64 > most)
         return RWKV7_ERR_SHAPE;
     return RWKV7_OK;
 }

@@ -617,3 +617,54 @@ def test_offsets_behind_32_bits(rnn):
     for name, a, b in zip(("dq", "dk", "dv"), grads, want):
         close(a[:, T:], f64(b), "bf16", name)
     close(grads[4][1], f64(want[4][0]), "f32", "ds0")
+
+
+@pytest.mark.parametrize("n,K,V", [(4096, 64, 64), (2048, 64, 256)])
+def test_large_batches(rnn, n, K, V):
+    """Prefill, gradients and single tokens of more sequences and heads than 2^18 - 1, against the same in two
+    halves (whole sequences, so bit for bit) and, for some, against float64."""
+    T, H = 2, 64
+    gen = torch.Generator("cuda").manual_seed(n)
+    new = lambda *shape: torch.randn(shape, device="cuda", generator=gen)  # noqa: E731
+    x = [new(n, T, H, C).bfloat16() for C in (K, K, V)] + [-torch.rand(H, device="cuda", generator=gen)]
+    s0, d_o, ds = new(n, H, V, K), new(n, T, H, V).bfloat16(), new(n, H, V, K)
+    halves = [slice(0, n // 2), slice(n // 2, n)]
+    part = lambda h: [t[h] for t in x[:3]] + [x[3]]  # noqa: E731
+    some = (0, n // 2, n - 1)
+
+    o, s = rnn.linear_attention_forward(*x, s0=s0)
+    for h in halves:
+        a, b = rnn.linear_attention_forward(*part(h), s0=s0[h])
+        assert torch.equal(o[h], a) and torch.equal(s[h], b)
+    for i in some:
+        want, S, _ = la.forward(*rows(x, i, 0, T), f64(s0[i]))
+        close(o[i], want, "bf16", "o")
+        close(s[i], S, "f32", "state")
+
+    one, pool = [t[:, 0].contiguous() for t in x[:3]], s0.clone()
+    od = rnn.linear_attention_decode(*one, x[3], pool)
+    for i in some:
+        want, S, _ = la.forward(*rows(x, i, 0, 1), f64(s0[i]))
+        close(od[i:i + 1], want, "bf16", "decode")
+        close(pool[i], S, "f32", "decoded state")
+    for h in halves:
+        again = s0[h].clone()
+        assert torch.equal(od[h], rnn.linear_attention_decode(*(t[h] for t in one), x[3], again))
+        assert torch.equal(pool[h], again)
+    del s, pool, again, a, b
+
+    grads = rnn.linear_attention_backward(*x, d_o, s0, ds)
+    dg = []
+    for h in halves:
+        got = rnn.linear_attention_backward(*part(h), d_o[h], s0[h], ds[h])
+        for name, a, b in zip(("dq", "dk", "dv", "", "ds0"), grads, got):
+            assert not name or torch.equal(a[h], b), name
+        dg.append(got[3].double())
+    # sums in float64, each rounded once to float32
+    bound = 2.0 ** -24 * (grads[3].abs() + dg[0].abs() + dg[1].abs()) * 1.01
+    assert ((dg[0] + dg[1] - grads[3]).abs() <= bound).all()
+    picked = [tuple(t[i:i + 1] for i in some) for t in (grads[0], grads[1], grads[2], grads[4])]
+    for j, i in enumerate(some):
+        got = (*(t[j] for t in picked[:3]), None, picked[3][j])
+        check_gradients(got, [t[i:i + 1] for t in x[:3]] + [x[3]], d_o[i:i + 1], ds[i:i + 1], s0[i:i + 1], "bf16",
+                        [(0, 0, T)])

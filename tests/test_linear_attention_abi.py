@@ -212,3 +212,17 @@ def test_binding_refuses_wrong_gates_and_types():
         with pytest.raises(ValueError, match="2\\^31"):
             f(2 ** 32 + 64, 1, 1, 64, 64)
         assert f(-1, 1, 1, 64, 64) == 0
+
+
+@pytest.mark.parametrize("heads,K,V", [(64, 64, 64), (64, 128, 256), (64, 64, 192), (32, 128, 128)])
+def test_large_batches_are_taken(heads, K, V):
+    """All whose states are below 2^38 bytes, whole or in segments."""
+    sequences = 2 ** 38 // (4 * heads * K * V)
+    sequences -= 2 ** 38 % (4 * heads * K * V) == 0
+    size = lambda n, packed: rnn.linear_attention_backward_workspace_bytes(  # noqa: E731
+        n, heads, heads, K, V, sequences=n, packed=packed)
+    parts = {64: 1, 128: 1, 192: 3, 256: 2}[V]
+    for n in (2048, 4096, 8192, sequences):
+        for packed in (False, True):  # (a number for dg for each, and where V is in parts gradients to add)
+            assert size(n, packed) == n * heads * parts * 8 + (2 * n * heads * parts * K * 4 if parts > 1 else 0)
+    assert size(sequences + 1, False) == 0
