@@ -957,7 +957,8 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
     dq.direct = kStart;
     dq.cotangent = b.ds_T;
     dq.unit_cotangents = b.cotangents;
-    const Direct from_end = b.ds0 && b.ds0 == b.ds_T ? kNone : kStart;  // (dk reads what dv writes)
+    const bool in_place = b.ds0 && b.ds0 == b.ds_T;  // dk reads what dv writes
+    const Direct from_end = in_place ? kNone : kStart;
     dq.direct_end = from_end == kStart;
     dq.dg = b.dg_units;
 
@@ -1005,7 +1006,7 @@ hipError_t launch_backward(const BackwardArgs &b, hipStream_t stream) {
     // is a launch of its own in bf16, where it has half as many waves on a SIMD as the others; in
     // float they are equal.  ds_T and ds0 may be the same memory: then dv, which writes ds0, is
     // launched behind those that read ds_T.
-    const bool alike = p.K == p.V && (!wide || !p.bf16) && (b.seg.seg || b.ds0 != b.ds_T);
+    const bool alike = p.K == p.V && (!wide || !p.bf16) && (b.seg.seg || !in_place);
     int n = 0;
     if (b.dg_units && alike && !p.bf16) {
         a.pass[n++] = dq;

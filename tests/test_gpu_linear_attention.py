@@ -9,6 +9,8 @@ Tolerances (2-norm of the difference over that of the result, unless stated):
  - dg adds products of either sign: per element of the state the sum over tokens of |D S|, independent
    between elements, each off by the errors of D and S, 2e-6 = 32 * 2^-24 of it.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -668,3 +670,34 @@ def test_large_batches(rnn, n, K, V):
         got = (*(t[j] for t in picked[:3]), None, picked[3][j])
         check_gradients(got, [t[i:i + 1] for t in x[:3]] + [x[3]], d_o[i:i + 1], ds[i:i + 1], s0[i:i + 1], "bf16",
                         [(0, 0, T)])
+
+
+def launches(call):
+    """Kernels that the call enqueues: the nodes of a graph that it is captured into."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    count = ctypes.c_size_t()
+    nodes = ctypes.CDLL("libamdhip64.so").hipGraphGetNodes
+    assert nodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(count)) == 0
+    return count.value
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_without_the_final_states_are_launched_together(rnn, dtype):
+    """No cotangent of the final states and no gradient of the first ones: nothing is in another's place, and
+    the launches and results are those of zeros; only ds0 in ds_T's place takes one more launch."""
+    T, H, K, V = 100, 2, 64, 64
+    x = inputs(T, H, H, K, V, dtype, 14)
+    d_o = torch.from_numpy(np.random.default_rng(15).normal(size=(1, T, H, V))).to(DT[dtype]).cuda()
+    zeros, ds0 = torch.zeros(1, H, V, K, device="cuda"), torch.empty(1, H, V, K, device="cuda")
+    without = lambda: rnn.linear_attention_backward(*x, d_o, want_ds0=False)  # noqa: E731
+    apart = lambda: rnn.linear_attention_backward(*x, d_o, None, zeros, ds0=ds0)  # noqa: E731
+    for a, b in zip(without()[:4], apart()):
+        assert torch.equal(a, b)
+    same = ds0.clone()
+    same.zero_()
+    in_place = lambda: rnn.linear_attention_backward(*x, d_o, None, same, ds0=same)  # noqa: E731
+    in_place()
+    assert torch.equal(same, ds0)
+    assert launches(without) == launches(apart) < launches(in_place)
