@@ -701,3 +701,57 @@ def test_gradients_without_the_final_states_are_launched_together(rnn, dtype):
     in_place()
     assert torch.equal(same, ds0)
     assert launches(without) == launches(apart) < launches(in_place)
+
+
+def backward_segments(rnn, T, H, K, V, dtype):
+    """Segments that the gradients of one dense sequence are computed in, from the workspace's size (a state and
+    a cotangent of each, and 8 bytes for dg)."""
+    size = rnn.linear_attention_backward_workspace_bytes(T, H, H, K, V, dtype=dtype)
+    one = H * (2 * V * K * 4 + 8)
+    return size // one if size % one == 0 else 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("T,H,count", [(193, 1, 4), (250, 3, 4), (450, 40, 4), (270, 64, 3), (384, 50, 3)])
+@pytest.mark.parametrize("started", [True, False])
+def test_three_and_four_segments_joined_in_the_backward(rnn, dtype, K, V, T, H, count, started):
+    """Of one and two chunks, the last one short or whole; heads that keep nearly everything, and others."""
+    assert backward_segments(rnn, T, H, K, V, dtype) == count
+    x = inputs(T, H, H, K, V, dtype, 16 + T)
+    x[3][0] = -1e-3
+    if H > 1:
+        x[3][1] = 0.0
+    s0, ds = (states(1, H, V, K, 3), states(1, H, V, K, 4)) if started else (None, None)
+    d_o = torch.from_numpy(np.random.default_rng(17).normal(size=(1, T, H, V))).to(DT[dtype]).cuda()
+    grads = rnn.linear_attention_backward(*x, d_o, s0, ds)
+    some = sorted({0, min(1, H - 1), H - 1})
+    of = lambda t: None if t is None else t[:, some]  # noqa: E731
+    picked = [t[:, :, some] for t in grads[:3]] + [grads[3][some], of(grads[4])]
+    check_gradients(picked, [t[:, :, some] for t in x[:3]] + [x[3][some]], d_o[:, :, some], of(ds), of(s0), dtype,
+                    [(0, 0, T)])
+    fixed = rnn.linear_attention_backward(*x, d_o, s0, ds, want_dg=False)
+    assert fixed[3] is None
+    for a, b, n in zip(fixed, grads, ("dq", "dk", "dv", "", "ds0")):
+        if n:  # (dq takes the state in two parts where dg is not wanted, else in three)
+            close(a, f64(b), dtype, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,count", [(700, 60, 2), (500, 40, 3), (1100, 30, 4)])
+def test_joined_segments_with_slots(rnn, dtype, T, H, count):
+    """Dense sequences from one pool into another, whose entries are in another order; one starts from zeros."""
+    B, K, V = 2, 64, 128
+    size = rnn.linear_attention_forward_workspace_bytes(B * T, H, H, K, V, sequences=B, dtype=dtype)
+    assert size == count * B * H * V * K * 4
+    x = inputs(B * T, H, H, K, V, dtype, 18, B)
+    x[3][0], x[3][1] = 0.0, -1e-3
+    pool, out = states(4, H, V, K, 5), torch.full((4, H, V, K), 7.0, device="cuda")
+    o, _ = rnn.linear_attention_forward(*x, s0=pool, s_out=out, slots=t32([3, 0]), slots_in=t32([1, -1]))
+    some = [0, 1, H - 1]
+    for b, (start, end) in enumerate(((1, 3), (None, 0))):
+        r = rows([t[:, :, some] for t in x[:3]] + [x[3][some]], b, 0, T)
+        want, S, _ = la.forward(*r, None if start is None else f64(pool[start][some]))
+        close(o[b][:, some], want, dtype, "o")
+        close(out[end][some], S, "f32", "state")
+    assert (out[1:3] == 7).all()
