@@ -755,3 +755,36 @@ def test_joined_segments_with_slots(rnn, dtype, T, H, count):
         close(o[b][:, some], want, dtype, "o")
         close(out[end][some], S, "f32", "state")
     assert (out[1:3] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_long_prompt_among_single_tokens(rnn, dtype):
+    """A serving step's batch of one prompt and nine sequences that go on by a token (and an empty one), through a
+    pool and with gradients: right, and the same bits each time."""
+    Hk, Hv, K, V = 16, 32, 64, 64
+    lens = [1, 1, 1, 1100, 1, 0, 1, 1, 1, 1, 1]
+    n, cu = len(lens), np.cumsum([0] + lens)
+    x = inputs(cu[-1], Hk, Hv, K, V, dtype, 19)
+    x[3][0] = -1e-3
+    start, ds = states(n + 3, Hv, V, K, 6), states(n, Hv, V, K, 7)
+    slots = list(np.random.default_rng(20).permutation(n + 3)[:n])
+    d_o = torch.from_numpy(np.random.default_rng(21).normal(size=(1, cu[-1], Hv, V))).to(DT[dtype]).cuda()
+    first = None
+    for _ in range(3):
+        pool = start.clone()
+        o, _ = rnn.linear_attention_forward(*x, s0=pool, s_out=pool, slots=t32(slots), cu_seqlens=t32(cu))
+        s0 = start[slots].contiguous()
+        got = (o, pool, *rnn.linear_attention_backward(*x, d_o, s0, ds, cu_seqlens=t32(cu)))
+        first = got if first is None else first
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+    # key heads 0 and 15, with the value heads that read them
+    ks, vs = [0, Hk - 1], [0, 1, Hv - 2, Hv - 1]
+    y = [x[0][:, :, ks], x[1][:, :, ks], x[2][:, :, vs], x[3][vs]]
+    for i in range(n):
+        want, S, _ = la.forward(*rows(y, 0, cu[i], cu[i + 1]), f64(s0[i][vs]))
+        close(o[0, cu[i]:cu[i + 1]][:, vs], want, dtype, f"o of {i}")
+        close(pool[slots[i]][vs], S, "f32", f"state of {i}")
+    for i in set(range(n + 3)) - set(slots):
+        assert torch.equal(pool[i], start[i])
+    grads = [got[2][:, :, ks], got[3][:, :, ks], got[4][:, :, vs], got[5][vs], got[6][:, vs]]
+    check_gradients(grads, y, d_o[:, :, vs], ds[:, vs], s0[:, vs], dtype, [(0, cu[i], cu[i + 1]) for i in range(n)])
