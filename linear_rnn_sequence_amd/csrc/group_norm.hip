@@ -141,8 +141,8 @@ struct Lane {
 
 // the statistics of a row: afterwards x holds u
 template <int VEC, int L, int NV, bool FULL>
-__device__ __forceinline__ void normalize(float (&x)[VEC * NV], float &rstd, const Lane<VEC, L, NV, FULL> &at,
-                                          const Args &a) {
+__device__ __forceinline__ void normalize(float (&x)[VEC * NV], float &rstd,
+                                          const Lane<VEC, L, NV, FULL> &at, const Args &a) {
     constexpr int N = VEC * NV;
     float mean = 0.f, var = 0.f;
 #pragma unroll
@@ -242,7 +242,8 @@ __global__ __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 4 : 1) void backwar
     const E *xp = static_cast<const E *>(a.x) + first * a.x_stride,
             *gp = static_cast<const E *>(a.gate) + (GATE ? first * a.gate_stride : 0),
             *dp = static_cast<const E *>(a.dy) + first * C;
-    E *dxp = static_cast<E *>(a.dx) + first * C, *dzp = static_cast<E *>(a.dgate) + (GATE ? first * C : 0);
+    E *dxp = static_cast<E *>(a.dx) + first * C,
+      *dzp = static_cast<E *>(a.dgate) + (GATE ? first * C : 0);
     float dw[N], db[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
@@ -469,8 +470,10 @@ int piece(const Args &a, int esz, std::initializer_list<const void *> ps) {
 template <class E, int VEC, int L, int NV, bool FULL>
 void (*kernel_of(const Args &a, bool backward))(Args) {
     if (backward)
-        return a.gate ? &backward_kernel<E, VEC, L, NV, true, FULL> : &backward_kernel<E, VEC, L, NV, false, FULL>;
-    return a.gate ? &forward_kernel<E, VEC, L, NV, true, FULL> : &forward_kernel<E, VEC, L, NV, false, FULL>;
+        return a.gate ? &backward_kernel<E, VEC, L, NV, true, FULL>
+                      : &backward_kernel<E, VEC, L, NV, false, FULL>;
+    return a.gate ? &forward_kernel<E, VEC, L, NV, true, FULL>
+                  : &forward_kernel<E, VEC, L, NV, false, FULL>;
 }
 template <class E, int VEC, int L, int NV>
 hipError_t launch(Args a, bool backward, hipStream_t stream) {
@@ -512,7 +515,8 @@ hipError_t launch(const Args &a, bool backward, hipStream_t stream) {
 }
 hipError_t launch(const Args &a, int esz, int vec, bool backward, hipStream_t stream) {
     if (a.rows == 0) return hipSuccess;
-    if (esz == 4) return vec == 4 ? launch<float, 4>(a, backward, stream) : launch<float, 1>(a, backward, stream);
+    if (esz == 4)
+        return vec == 4 ? launch<float, 4>(a, backward, stream) : launch<float, 1>(a, backward, stream);
     if (vec == 8) return launch<uint16_t, 8>(a, backward, stream);
     return vec == 2 ? launch<uint16_t, 2>(a, backward, stream) : launch<uint16_t, 1>(a, backward, stream);
 }
@@ -538,7 +542,8 @@ rwkv7_status group_norm_forward(const group_norm_problem *in, const void *x, con
     Args &a = c.a;
     if (a.rows > 0 && (!x || !y)) return RWKV7_ERR_NULL;
     const size_t esz = (size_t)c.esz;
-    if (!aligned(x, esz) || !aligned(gate, esz) || !aligned(y, esz) || !aligned(weight, 4) || !aligned(bias, 4))
+    if (!aligned(x, esz) || !aligned(gate, esz) || !aligned(y, esz) || !aligned(weight, 4) ||
+        !aligned(bias, 4))
         return RWKV7_ERR_ALIGN;
     const long long C = (long long)a.groups * a.size;
     const size_t params = (size_t)C * 4;
@@ -577,8 +582,9 @@ rwkv7_status group_norm_backward(const group_norm_problem *in, const void *x, co
     if (!aligned(workspace, 16)) return RWKV7_ERR_ALIGN;
     const size_t params = (size_t)C * 4, dense = extent(a.rows, C, C, c.esz);
     if (!disjoint({{dx, dense}, {dgate, dense}, {dweight, params}, {dbias, params}, {workspace, need}},
-                  {{x, extent(a.rows, a.x_stride, C, c.esz)}, {gate, extent(a.rows, a.gate_stride, C, c.esz)},
-                   {weight, params}, {bias, params}, {dx == dy ? nullptr : dy, dense}}))
+                  {{x, extent(a.rows, a.x_stride, C, c.esz)},
+                   {gate, extent(a.rows, a.gate_stride, C, c.esz)}, {weight, params}, {bias, params},
+                   {dx == dy ? nullptr : dy, dense}}))
         return RWKV7_ERR_ALIAS;
     a.x = x; a.gate = gate; a.weight = weight; a.bias = bias; a.dy = dy;
     a.dx = dx; a.dgate = dgate;

@@ -122,7 +122,9 @@ struct Plane {
     static constexpr int kBytes = kChunk * kRow;
     char *p;
     // a lane's place for reads along the rows: row lo, channels 8 g ..
-    static __device__ __forceinline__ int along(int g, int lo) { return lo * kRow + 8 * g * (int)sizeof(E); }
+    static __device__ __forceinline__ int along(int g, int lo) {
+        return lo * kRow + 8 * g * (int)sizeof(E);
+    }
     // channels 32 ks + 8 g .. of row 16 i + lo; `at`: p + along()
     static __device__ __forceinline__ Frag<E> rows(const char *at, int i, int ks) {
         at += 16 * i * kRow + 32 * ks * (int)sizeof(E);
@@ -151,9 +153,11 @@ struct Plane {
         if constexpr (sizeof(E) == 2) {
             typedef short s4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s4 lds_s4;
-            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at)),
-                        b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                          (lds_s4 *)(at + 16 * kRow)));
+            auto read = [](const char *from) {
+                return __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)from));
+            };
+            const u32x2 a = read(at), b = read(at + 16 * kRow);
             f.v = u32x4{a[0], a[1], b[0], b[1]};
         } else {
 #pragma unroll
@@ -190,7 +194,8 @@ template <class E, int C, int THREADS>
 struct Rows {
     static constexpr int kPiece = 16 / (int)sizeof(E), kRowPieces = C / kPiece;  // elements, per row
     static constexpr int kPer = kChunk * kRowPieces / THREADS, kStep = THREADS / kRowPieces;
-    static_assert(THREADS % kRowPieces == 0 && kPer * kStep == kChunk, "a thread's pieces are kStep rows apart");
+    static_assert(THREADS % kRowPieces == 0 && kPer * kStep == kChunk,
+                  "a thread's pieces are kStep rows apart");
     u32x4 d[kPer];
     static __device__ __forceinline__ unsigned offset(int row, int col, int stride, int live,
                                                       bool reverse) {
@@ -299,15 +304,18 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
     } else {
         sq = a.lay.seq(unit, kChunk);
     }
-    const int tokens = sq.end - sq.begin, rest = tokens - first, len = a.seg && rest > a.seg ? a.seg : rest;
-    const bool ends = reverse ? first == 0 : len == rest, starts = reverse ? len == rest : first == 0;
+    const int tokens = sq.end - sq.begin, rest = tokens - first;
+    const int len = a.seg && rest > a.seg ? a.seg : rest;
+    const bool ends = reverse ? first == 0 : len == rest;
+    const bool starts = reverse ? len == rest : first == 0;
     if (MODE == kSum && ends) return;  // nothing follows it
     const long long token = (long long)sq.begin + first;
     const int chunks = (len + kChunk - 1) / kChunk;
     const size_t state_size = (size_t)VD * KD;
 
     const Decay decay(a.g[h / a.parts]);
-    float *write = reinterpret_cast<float *>(lds + L::kWrite), *pairs = reinterpret_cast<float *>(lds + L::kPair),
+    float *write = reinterpret_cast<float *>(lds + L::kWrite),
+          *pairs = reinterpret_cast<float *>(lds + L::kPair),
           *reads = reinterpret_cast<float *>(lds + L::kReads);
     if (tid < kChunk) {
         write[tid] = p.write * decay.power(kChunk - p.shift - tid);
@@ -379,7 +387,8 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
 
     using PK = Plane<E, KD>;
     using PV = Plane<E, VD>;
-    char *const px = lds + L::kX, *const py = lds + L::kY, *const pz = lds + L::kZ, *const pe = lds + L::kE;
+    char *const px = lds + L::kX, *const py = lds + L::kY;
+    char *const pz = lds + L::kZ, *const pe = lds + L::kE;
     const char *const x_rows = px + PK::along(g, lo), *const y_rows = py + PK::along(g, lo),
                *const y_cols = py + PK::template down<8>(g, lo),
                *const z_cols = pz + PV::template down<4>(g, lo) + own0 * (int)sizeof(E),
@@ -480,7 +489,8 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n)
-                    if (mine(n)) d[n] = mma(PK::rows(y_rows, jt[n], ks), PK::rows(x_rows, it[n], ks), d[n]);
+                    if (mine(n))
+                        d[n] = mma(PK::rows(y_rows, jt[n], ks), PK::rows(x_rows, it[n], ks), d[n]);
             if constexpr (MODE == kGrad) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -586,8 +596,10 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
             zs[st] = Parts<E, 3>(w[0], w[1]);
             if constexpr (MODE == kGrad) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j >> 2][j & 3] *= (float)(live - p.shift - (32 * st + 4 * g + (j < 4 ? j : 12 + j)));
+                for (int j = 0; j < 8; ++j) {
+                    const int token = 32 * st + 4 * g + (j < 4 ? j : 12 + j);
+                    w[j >> 2][j & 3] *= (float)(live - p.shift - token);
+                }
                 zr[st] = Parts<E, 3>(w[0], w[1]);
             }
         };
@@ -630,28 +642,31 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
             // tokens, 40 heads of 64)
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                    const f32x4 &x = out[i], &y = out[i + 1];
-                    if constexpr (sizeof(E) == 2) {
-                        // Neighbouring lane groups trade the halves of two tiles (v_permlane16_swap:
-                        // the odd ones' of its first operand for the even ones' of its second), so
-                        // that a lane has eight values of a token: even groups of tile i, odd ones
-                        // of i + 1.  (Writes of 8 bytes meet the same banks: 16 cycles for 5.)
-                        const auto u = __builtin_amdgcn_permlane16_swap(cvt_pk(x[0], x[1]), cvt_pk(y[0], y[1]), false, false);
-                        const auto v = __builtin_amdgcn_permlane16_swap(cvt_pk(x[2], x[3]), cvt_pk(y[2], y[3]), false, false);
-                        *reinterpret_cast<u32x4 *>(pz + pair_place + 16 * i * PV::kRow) =
-                            u32x4{u[0], v[0], u[1], v[1]};
-                    } else {
-                        char *at = pz + own_place + 16 * i * PV::kRow;
-                        *reinterpret_cast<f32x4 *>(at) = x;
-                        *reinterpret_cast<f32x4 *>(at + 16 * PV::kRow) = y;
-                    }
+                const f32x4 &x = out[i], &y = out[i + 1];
+                if constexpr (sizeof(E) == 2) {
+                    // Neighbouring lane groups trade the halves of two tiles (v_permlane16_swap:
+                    // the odd ones' of its first operand for the even ones' of its second), so
+                    // that a lane has eight values of a token: even groups of tile i, odd ones
+                    // of i + 1.  (Writes of 8 bytes meet the same banks: 16 cycles for 5.)
+                    const auto u = __builtin_amdgcn_permlane16_swap(
+                        cvt_pk(x[0], x[1]), cvt_pk(y[0], y[1]), false, false);
+                    const auto v = __builtin_amdgcn_permlane16_swap(
+                        cvt_pk(x[2], x[3]), cvt_pk(y[2], y[3]), false, false);
+                    *reinterpret_cast<u32x4 *>(pz + pair_place + 16 * i * PV::kRow) =
+                        u32x4{u[0], v[0], u[1], v[1]};
+                } else {
+                    char *at = pz + own_place + 16 * i * PV::kRow;
+                    *reinterpret_cast<f32x4 *>(at) = x;
+                    *reinterpret_cast<f32x4 *>(at + 16 * PV::kRow) = y;
                 }
+            }
         }
         if constexpr (MODE != kSum && sizeof(O) != sizeof(E)) {
             const Buffer b(op + start_of(c) * row, row_bytes<O>(live, row));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 4 * g, row, live, reverse), out[i], O());
+                b.store4(Rows<O, VD, kThreads>::offset(16 * i + lo, own0 + 4 * g, row, live, reverse),
+                         out[i], O());
         }
         // the state, kGroup tiles of columns at a time; beside the products the next group's rows of y
         // are on their way, its tiles are decayed, and the second half's z is split
@@ -678,7 +693,8 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
         }
         __syncthreads();  // out is whole, and the planes have been read
         if constexpr (MODE != kSum && sizeof(O) == sizeof(E))
-            Rows<E, VD, kThreads>::store(pz, reinterpret_cast<E *>(op + start_of(c) * row), row, live, reverse, tid);
+            Rows<E, VD, kThreads>::store(pz, reinterpret_cast<E *>(op + start_of(c) * row), row, live,
+                                         reverse, tid);
         if constexpr (MODE == kGrad) dg += dg_chunk;
         if (!L::kAhead) fetch(c + 1);
         put();
@@ -727,13 +743,15 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
 }
 
 template <class E, class O, int KD, int VD, Mode MODE>
-__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads), (Shared<E, KD, VD, MODE>::kPerSimd)) void pass_kernel(
-    PassArgs a) {
+__global__ __launch_bounds__((Shared<E, KD, VD, MODE>::kThreads),
+                             (Shared<E, KD, VD, MODE>::kPerSimd)) void
+pass_kernel(PassArgs a) {
     run_pass<E, O, KD, VD, MODE>(a, a.pass[blockIdx.y]);
 }
 // dq with dg, and the passes behind it, in one launch
 template <class E, class O, int KD, int VD>
-__global__ __launch_bounds__((Shared<E, KD, VD, kGrad>::kThreads), (Shared<E, KD, VD, kGrad>::kPerSimd)) void
+__global__ __launch_bounds__((Shared<E, KD, VD, kGrad>::kThreads),
+                             (Shared<E, KD, VD, kGrad>::kPerSimd)) void
 gradient_kernel(PassArgs a) {
     if (blockIdx.y == 0)
         run_pass<E, O, KD, VD, kGrad>(a, a.pass[0]);
@@ -856,8 +874,8 @@ hipError_t launch_pass(const PassArgs &a, int units, int passes, hipStream_t str
     const hipError_t e = allow_lds(kernel, L::kBytes);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((pass_kernel<E, O, KD, VD, MODE>),
-                       dim3((unsigned)((size_t)units * a.heads), (unsigned)passes), dim3(L::kThreads), L::kBytes,
-                       stream, a);
+                       dim3((unsigned)((size_t)units * a.heads), (unsigned)passes),
+                       dim3(L::kThreads), L::kBytes, stream, a);
     return hipGetLastError();
 }
 template <int D>
@@ -866,8 +884,9 @@ hipError_t launch_gradients(const PassArgs &a, int units, hipStream_t stream) {
     const hipError_t e =
         allow_lds(reinterpret_cast<const void *>(&gradient_kernel<float, float, D, D>), L::kBytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gradient_kernel<float, float, D, D>), dim3((unsigned)((size_t)units * a.heads), 3),
-                       dim3(L::kThreads), L::kBytes, stream, a);
+    hipLaunchKernelGGL((gradient_kernel<float, float, D, D>),
+                       dim3((unsigned)((size_t)units * a.heads), 3), dim3(L::kThreads), L::kBytes,
+                       stream, a);
     return hipGetLastError();
 }
 template <class E, class O, Mode MODE>
