@@ -25,7 +25,10 @@
  *    a row are dense, and so are all other tensors.
  *  - Numerics: float32 throughout, the variance from the differences to the mean; outputs are
  *    rounded once to dt.  The same call gives the same bits.  Sums of squares must be finite
- *    in float32.
+ *    in float32.  With bf16 rows the sigmoid of act is off by up to 2^-22 of itself, and for
+ *    a negative argument z by 1.25 |z| 2^-24 more, in the float32 gradients of weight and bias
+ *    as well.  Its derivative is off by 2^-22 of 1 (float32 rows too): a sigmoid gate beyond 17
+ *    gets the gradient 0.
  *  - Non-finite inputs stay in their row and group (and in the gradients of their channels'
  *    weight and bias).
  */
@@ -38,12 +41,16 @@
 extern "C" {
 #endif
 
-typedef enum { GROUP_NORM_NONE = 0, GROUP_NORM_SILU = 1, GROUP_NORM_SIGMOID = 2 } group_norm_activation;
+typedef enum {
+    GROUP_NORM_NONE = 0,
+    GROUP_NORM_SILU = 1,
+    GROUP_NORM_SIGMOID = 2
+} group_norm_activation;
 
 typedef struct {
     long long rows;         /* >= 0, at most 2^31 - 1                                    */
     int groups, size;       /* groups * size at most 2^23                                */
-    long long x_stride;     /* elements from row to row; 0: C.  At least C               */
+    long long x_stride;     /* elements from row to row; 0: C.  At least C, at most 2^23 */
     long long gate_stride;  /* likewise                                                  */
     float eps;
     group_norm_activation activation;

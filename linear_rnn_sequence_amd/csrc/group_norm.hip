@@ -97,14 +97,18 @@ __device__ __forceinline__ void channels(float (&x)[VEC * NV], const float *p, c
         for (int v = 0; v < NV; ++v) __builtin_memcpy(&x[v * VEC], p + col[v], VEC * sizeof(float));
 }
 
-// sigmoid; for outputs of 8 bits the hardware's exponential and reciprocal, 2^-22 off
+// sigmoid.  For rows of 8 bits the hardware's exponential and reciprocal: off by 2^-22 of itself, and
+// where x is negative by 1.25 |x| 2^-24 more, since the exponent log2(e) x is a float (2^-19.4 at
+// x = -20, 2^-17.4 at -80).  Outputs of bf16 are rounded by up to 2^-8; the float gradients of weight
+// and bias, formed from the same rows, take it as it is.
 template <class E>
 __device__ __forceinline__ float sigmoid(float x) {
     if constexpr (sizeof(E) == 2)
         return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
     return 1.f / (1.f + expf(-x));
 }
-// silu and sigmoid, and with them their derivatives; `silu` is the same for all lanes
+// silu and sigmoid, and with them their derivatives; `silu` is the same for all lanes.  (s - s^2 is
+// off by a few roundings of s: 2^-22 where s is close to 1, and 0 beyond x = 17.)
 template <class E>
 __device__ __forceinline__ float activate(float x, bool silu) {
     return sigmoid<E>(x) * (silu ? x : 1.f);

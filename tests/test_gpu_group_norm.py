@@ -372,3 +372,80 @@ def test_layer_captured_and_replayed(rnn):
             assert torch.equal(t, want[n]), n
         rnn.group_norm_forward(x[7], Hv)  # eager work between the replays
         torch.cuda.synchronize()
+
+
+def sigmoid_off(z, dtype):
+    """How far the sigmoid may be off, relative to itself.  float: the exponential's 2^-23, the sum's and the
+    quotient's 2^-24 each.  bf16: the hardware's exponential and reciprocal, 2^-23 each, and the sum's 2^-24; and the
+    exponent, log2(e) z, is a float whose product and constant are off by 2^-24 and 2^-26 of it, of which 1 - s
+    reaches the sigmoid (1.25 |z| 2^-24 log2(e) ln 2)."""
+    s = 1 / (1 + np.exp(-z))
+    return s, 2.0 ** -22 + 2.0 ** -24 + (1.25 * 2.0 ** -24 * np.abs(z) * (1 - s) if dtype == "bf16" else 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gradients_at_large_gates(rnn, dtype, act):
+    """Value by value, channels whose gates are far out in every row (so that their dweight and dbias are sums of
+    small terms only) beside ordinary ones; bounds from the roundings of each step."""
+    rows, groups, size = 16, 2, 128
+    x, dy, kw = inputs(rows, groups, size, dtype)
+    far = [-100.0, -80.0, -60.0, -20.0, -8.0, 8.0, 12.0, 17.0, 20.0, 60.0, 80.0, 100.0]
+    kw["gate"][:, 5:5 + len(far)] = torch.tensor(far).to(DT[dtype])
+    kw["gate"][:, 200] *= 50
+    ref = {n: f64(t) for n, t in kw.items()}
+    y, (dx, dw, db, dz) = (rnn.group_norm_forward(x, groups, activation=act, **kw),
+                           rnn.group_norm_backward(x, groups, dy, activation=act, **kw))
+    want_y = gn.forward(f64(x), groups, activation=act, **ref)
+    want = gn.backward(f64(x), groups, f64(dy), activation=act, **ref)
+
+    X, D, z, w = f64(x), np.abs(f64(dy)), ref["gate"], np.abs(ref["weight"])
+    unit, inv, n = gn._parts(X, groups, ref["weight"], ref["bias"], 1e-5, False)
+    group = lambda t: t.reshape(rows, groups, size)  # noqa: E731
+    flat = lambda t: t.reshape(rows, groups * size)  # noqa: E731
+    mean = lambda t: np.broadcast_to(t.mean(-1, keepdims=True), t.shape)  # noqa: E731
+    step, half = 2.0 ** -24, {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype]
+    u = np.abs(unit)
+    # u: sums of 128 terms as trees (12 roundings), of the squares too (half of it in rstd), rsqrtf 2^-22, the
+    # difference and the product: below 16 steps of |u| and of mean |x| rstd
+    u_off = 16 * step * (u + flat(mean(group(np.abs(X))) * inv))
+    n_off = w * u_off + 2 * step * (w * u + np.abs(n))
+    s, rel = sigmoid_off(z, dtype)
+    tiny = 2.0 ** -120  # the sigmoid's smallest normal values, times what it is multiplied with
+    s_off = rel * s
+    a, slope = gn._act(z, act)
+    if act == "silu":
+        a_off, slope_off = np.abs(z) * s_off + step * np.abs(a), (1 + np.abs(z)) * (s_off + 3 * step * s)
+    else:
+        a_off, slope_off = s_off, s_off + 3 * step * s
+    a, slope = np.abs(a), np.abs(slope)
+    off = {"y": a * n_off + np.abs(n) * a_off, "dgate": D * (slope * n_off + np.abs(n) * slope_off),
+           "dbias": (D * a_off).sum(0) + (rows + 1) * step * (D * a).sum(0),
+           "dweight": (D * (a_off * u + a * u_off)).sum(0) + (rows + 2) * step * (D * a * u).sum(0)}
+    du, du_off = group(D * a * w), group(w * D * a_off + 2 * step * D * a * w)
+    gu, gu_off = group(u), group(u_off)
+    terms = du + mean(du) + gu * mean(du * gu)
+    off["dx"] = flat(inv * (du_off + mean(du_off) + gu * mean(du_off * gu + du * gu_off) + gu_off * mean(du * gu)
+                            + 32 * step * terms))
+    for name, got, exact, kind in (("y", y, want_y, dtype), ("dgate", dz, want[3], dtype), ("dx", dx, want[0], dtype),
+                                   ("dweight", dw, want[1], "f32"), ("dbias", db, want[2], "f32")):
+        last = half if kind == dtype else step
+        bound = off[name] * 1.01 + (last + 2 * step) * np.abs(exact) + tiny
+        bad = np.abs(f64(got) - exact) / bound
+        assert bad.max() <= 1, (name, bad.max(), np.unravel_index(bad.argmax(), bad.shape))
+    assert db[5 + far.index(-60.0)].abs() > 0 and (act == "silu" or db[5 + far.index(-80.0)].abs() > 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_outputs_at_the_largest_gates_are_finite_where_exact_ones_are(rnn, dtype, act):
+    x, _, kw = inputs(16, 2, 128, dtype)
+    ends = torch.tensor([1e30, -1e30, 3e38, -3e38, 200.0, -200.0, 89.0, -89.0]).to(DT[dtype])
+    kw["gate"][:, 30:30 + len(ends)] = ends
+    want = gn.forward(f64(x), 2, activation=act, **{n: f64(t) for n, t in kw.items()})
+    fine = torch.from_numpy(want).to(DT[dtype]).isfinite().numpy()
+    assert not fine.all() if act == "silu" else fine.all()
+    y = rnn.group_norm_forward(x, 2, activation=act, **kw)
+    assert np.array_equal(y.isfinite().cpu().numpy(), fine)
+    close(torch.where(torch.from_numpy(fine).cuda() & (kw["gate"].abs() < 300), y, torch.zeros_like(y)),
+          np.where(fine & (np.abs(f64(kw["gate"])) < 300), want, 0.0), dtype, "y")
