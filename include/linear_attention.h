@@ -48,9 +48,12 @@
  *    whether its states are updated in place.
  *  - A workspace serves one call at a time: calls, or captured graphs, that may run at once
  *    need one each.  What it held before does not matter.
- *  - Non-finite inputs propagate within a (sequence, value head) pair, and from q and k to all
- *    value heads of their key head; tokens of the same 64-token chunk before the non-finite
- *    one may become non-finite too, earlier chunks do not (decode works on single tokens).
+ *  - Non-finite inputs propagate within a (sequence, value head) pair, from q and k to all
+ *    value heads of their key head, and in the gradients of v's and d_o's to the key head.
+ *    In o and dq, tokens of the same 64-token chunk before the non-finite one may become
+ *    non-finite too, earlier chunks do not (decode works on single tokens).  dk and dv are
+ *    computed from the last token on: likewise, with the order of the tokens turned round and
+ *    the chunks counted from the end (of a segment, where the call has some).
  */
 #ifndef LINEAR_ATTENTION_H
 #define LINEAR_ATTENTION_H

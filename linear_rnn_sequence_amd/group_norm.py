@@ -6,7 +6,8 @@ the memory of a call these functions share.
 Shapes: x and gate [..., C] in one dtype (torch.bfloat16 or torch.float32), channels last, each row
 (token) normalised by itself in ``groups`` groups of C / groups neighbouring channels; weight and
 bias float32 [C].  x and gate may be slices of a joint projection: dense channels, rows equally
-spaced, at most 2^23 elements from one to the next.  The readouts [B,T,Hv,V] of a recurrence are ``o.flatten(-2)`` with ``groups=Hv``.
+spaced, at most 2^23 elements from one to the next.  The readouts [B,T,Hv,V] of a recurrence are
+``o.flatten(-2)`` with ``groups=Hv``.
 """
 from __future__ import annotations
 

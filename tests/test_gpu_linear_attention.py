@@ -788,3 +788,29 @@ def test_one_long_prompt_among_single_tokens(rnn, dtype):
         assert torch.equal(pool[i], start[i])
     grads = [got[2][:, :, ks], got[3][:, :, ks], got[4][:, :, vs], got[5][vs], got[6][:, vs]]
     check_gradients(grads, y, d_o[:, :, vs], ds[:, vs], s0[:, vs], dtype, [(0, cu[i], cu[i + 1]) for i in range(n)])
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "d_o"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_what_is_not_finite_stay_in_their_heads(rnn, dtype, name):
+    """And dq at and behind its chunk, dk and dv at and before it, their chunks counted from the end."""
+    B, T, Hk, Hv, K, V, at = 2, 180, 2, 4, 64, 64, 100
+    x = inputs(B * T, Hk, Hv, K, V, dtype, 23, B=B)
+    s0, ds = states(B, Hv, V, K, 1), states(B, Hv, V, K, 2)
+    d_o = torch.from_numpy(np.random.default_rng(24).normal(size=(B, T, Hv, V))).to(DT[dtype]).cuda()
+    clean = rnn.linear_attention_backward(*x, d_o, s0, ds)
+    (d_o if name == "d_o" else x["qkv".index(name)])[0, at, 1, 5] = float("nan")
+    key, hit = (1, [2, 3]) if name in "qk" else (0, [1])
+    keep = [h for h in range(Hv) if h not in hit]
+    got = rnn.linear_attention_backward(*x, d_o, s0, ds)
+    dq, dk, dv, dg, ds0 = zip(got, clean)
+    for a, b in (dq, dk, dv, ds0):
+        assert torch.equal(a[1], b[1])
+    for a, b in (dq, dk):
+        assert torch.equal(a[0][:, 1 - key], b[0][:, 1 - key])
+    assert torch.equal(dv[0][0][:, keep], dv[1][0][:, keep])
+    assert torch.equal(dg[0][keep], dg[1][keep]) and torch.equal(ds0[0][0][keep], ds0[1][0][keep])
+    assert torch.equal(dq[0][0, :64], dq[1][0, :64])
+    for a, b in (dk, dv):
+        assert torch.equal(a[0, T - 64:], b[0, T - 64:])
+    assert not all(dg[0][hit].isfinite())
