@@ -814,3 +814,25 @@ def test_gradients_of_what_is_not_finite_stay_in_their_heads(rnn, dtype, name):
     for a, b in (dk, dv):
         assert torch.equal(a[0, T - 64:], b[0, T - 64:])
     assert not all(dg[0][hit].isfinite())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [90, 400])  # whole, and in segments
+def test_growing_states(rnn, dtype, T):
+    """Log decays above 0 are computed as they stand."""
+    Hk, Hv, K, V = 1, 2, 64, 64
+    x = inputs(T, Hk, Hv, K, V, dtype, 25)
+    x[3][:] = torch.tensor([0.03, 1e-3])
+    s0, ds = states(1, Hv, V, K, 1), states(1, Hv, V, K, 2)
+    d_o = torch.from_numpy(np.random.default_rng(26).normal(size=(1, T, Hv, V))).to(DT[dtype]).cuda()
+    o, s = rnn.linear_attention_forward(*x, s0=s0)
+    want, S, _ = la.forward(*rows(x, 0, 0, T), f64(s0[0]))
+    for h in range(Hv):  # (the one that grows a thousandfold would hide the other)
+        close(o[0][:, h], want[:, h], dtype, "o")
+        close(s[0, h], S[h], "f32", "state")
+    check_gradients(rnn.linear_attention_backward(*x, d_o, s0, ds), x, d_o, ds, s0, dtype, [(0, 0, T)])
+    one, pool = [t[:, 0].contiguous() for t in x[:3]], s0.clone()
+    od = rnn.linear_attention_decode(*one, x[3], pool)
+    want, S, _ = la.forward(*rows(x, 0, 0, 1), f64(s0[0]))
+    close(od, want, dtype, "decode")
+    close(pool[0], S, "f32", "decoded state")
