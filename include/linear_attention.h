@@ -29,6 +29,9 @@
  *    access outside a buffer.
  *  - q, k and v may be strided from token to token (a slice of a joint projection); the
  *    channels of one token are dense [heads, K or V].
+ *  - A packed batch is planned by its tokens, its sequences and its heads; the lengths are on the
+ *    device.  One sequence that is far longer than the others, such as a prompt among single
+ *    tokens, is then a chain of all its chunks: it is several times faster in a call of its own.
  *  - The states of n_seq sequences take less than 2^38 bytes (also where none are given); Hv * V,
  *    and Hv * K times the parts of at most 128 values that V is computed in (192: three of 64), are
  *    at most 2^23.  Larger calls return RWKV7_ERR_SHAPE.

@@ -9,8 +9,8 @@
 // state load instruction of a wave reads whole rows (16 bytes per lane), and the readouts are
 // DPP reductions.  State accesses are non-temporal, each state is touched once per call.
 //
-// What bounds it: memory.  256 sequences of 32 heads of 128 x 128 (1.08 GB) take 177 us, 6.1 TB/s,
-// where a large copy reaches 6.6; one sequence 3.3 us, in a call that costs the host 11.
+// What bounds it: memory.  256 sequences of 32 heads of 128 x 128 (1.08 GB) take 176 us, 6.1 TB/s,
+// where a large copy reaches 6.6; one sequence 3.1 us, in a call that costs the host 11.
 #include "gated_delta_device.h"
 #include "linear_attention_internal.h"
 

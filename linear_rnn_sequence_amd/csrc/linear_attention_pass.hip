@@ -28,11 +28,12 @@
 // triangle, is computed by the waves together and passed through it.
 //
 // What bounds it: the instructions of a chunk, of which the products of states in two and three
-// bf16 parts are the largest share.  32768 tokens of 32 heads of 128 x 128 take 390 to 410 us (243 the
-// pass, 126 the segments' sums, 12 their combination; 1.1 GB at 4.6 TB/s in the pass): matrix cores are
-// busy 45% of the time, vector units 39%, shared memory 51%, waves wait 38% of theirs.  A chunk
-// takes 4.2 us of a CU, also where a batch's longest sequence is a chain of them (16 ragged
-// sequences of up to 2049 tokens: 152 to 162 us, 33 chunks).
+// bf16 parts are the largest share, and what its steps wait for each other.  32768 tokens of 32 heads
+// of 128 x 128 take 390 to 410 us (245 the pass, 125 the segments' sums, 12 their combination; 1.1 GB
+// at 4.6 TB/s in the pass): matrix cores are busy 46% of the time, vector units 40%, shared memory 51%,
+// waves wait 38% of theirs.  A chunk takes 4.2 us of a CU, also where a batch's longest sequence is a
+// chain of them (16 ragged sequences of up to 2049 tokens: 152 to 162 us, 33 chunks).  In float a large
+// call is at 1.6 to 3 times its operations' floor (8 x 2048 tokens of the same heads: 456 us).
 #include "gated_delta_device.h"
 #include "linear_attention_internal.h"
 
@@ -528,7 +529,10 @@ __device__ __forceinline__ void run_pass(const PassArgs &a, const Pass &p) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            // S x^T; the next step's operand is formed beside this one's products
+            // S x^T; the next step's operand is formed beside this one's products.  Two parts of the
+            // state, 16 bits, for outputs of 8: against sums in float one output in 430 is rounded the
+            // other way (16 ragged sequences of up to 2049 tokens), 1.0e-4 of them in the norm beside the
+            // rounding's own 1.7e-3.  Three for dg, whose terms cancel.
             constexpr int kRead = MODE == kGrad ? 3 : 2;
             f32x4 moved[4];
 #pragma unroll
@@ -1074,14 +1078,17 @@ constexpr int kFewSegments = 4;
 // How a call's sequences are cut into segments, which are then done in parallel.  A segment's
 // sum and the combination cost about half of the pass again, so whole sequences are taken where
 // they fill the card (256 workgroups; 8 x 4096 tokens, 40 heads of 64: 217 us whole, 255 in halves,
-// 296 in 256s) or are short (300 tokens, 32 heads of 128: 26 us whole, 30 in 64s, 25 in 128s).  Else
+// 296 in 256s) or are short (300 tokens, 32 heads of 128: 26 us whole, 31 in 64s, 29 in 128s; 384: 29
+// whole and in 128s, 32 in 64s; 448: 33 whole, 28 in 128s; 384 of 4 heads: 28 whole, 27 in 128s).  Else
 // about one workgroup per CU (2 x 1000 tokens, 32 heads of 128: 44 us, with two per CU 55; 2 x 4096:
 // 109 and 115; with gradients, 4 x 2048: 391 in 1024s, 450 in 512s, 477 whole; 4096 tokens, 16 heads:
 // 161 in 256s, 187 in 512s, 203 in 128s).  In the forward two, where one would have more than 2048
 // tokens (32768 tokens, 32 heads of 128: 402 us in 2048s, 424 in 4096s and in 1024s, 460 in 512s) or
 // has four waves (2 x 4096, 40 heads of 64: 64 us, with one per CU 73).  And not more segments than
 // their combination, a step of 0.25 us for each, is worth (6 us for a chunk more in each).  A packed
-// batch's longest sequence, which the host does not know, is taken for twice the mean.
+// batch's longest sequence, which the host does not know, is taken for twice the mean.  Where one is far
+// longer this is slow: 32768 tokens beside a single one, 32 heads of 128, take 979 us, beside eight 1946
+// (288 chains, all whole), for 408 alone; with gradients 5.3 ms for 1.25 beside eight.
 Segments plan_segments(const Problem &p, bool backward) {
     Segments s{0, p.n_seq, false};
     const long long chains = (long long)p.n_seq * p.heads;
